@@ -1,8 +1,8 @@
 """Thin ctypes binding over libpa.so with the C ABI's names.
 
 Argument marshalling only: shapes are read off the tensors, raw device
-pointers and sizes are passed to the C functions declared in include/pa.h,
-and a non-OK status raises ``PAError``.  Every step of the path runs in the
+pointers and sizes are passed to the C functions declared in include/pa.h and
+include/pa_window.h, and a non-OK status raises ``PAError``.  Every step of the path runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback, and loading
 fails loudly when libpa.so is missing.
 """
@@ -24,8 +24,9 @@ PA_DEVERR_CONTEXT_LEN = 2
 PA_DEVERR_SLOT = 4
 PA_DEVERR_COPY_PAIR = 8
 PA_DEVERR_TIMEOUT = 16
+PA_DEVERR_POSITION = 32
 
-# every symbol include/pa.h declares
+# every symbol the headers in include/ declare
 EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_workspace_init",
             "pa_decode", "pa_copy_blocks", "pa_status_string",
             "pa_get_last_device_error", "pa_decode_no_alloc", "pa_selftest_bounded_wait",
@@ -36,7 +37,9 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_works
             "pa_copy_blocks_raw", "pa_prefill", "pa_swap_blocks", "pa_bm_create_with_swap",
             "pa_bm_num_free_cpu", "pa_bm_cpu_refcount", "pa_bm_is_swapped", "pa_bm_swap_out",
             "pa_bm_swap_in", "pa_decode_append", "pa_decode_grouped_workspace_size",
-            "pa_decode_grouped", "pa_decode_contiguous")
+            "pa_decode_grouped", "pa_decode_contiguous", "pa_rope_and_cache",
+            "pa_rope_and_cache_q8", "pa_decode_window_workspace_size", "pa_decode_window",
+            "pa_decode_q8")
 
 _lock = threading.Lock()
 _lib = None
@@ -131,6 +134,21 @@ def load(path: str | None = None):
         lib.pa_prefill.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
                                    i32, i32, ctypes.c_float, vp]
         lib.pa_prefill.restype = i32
+        f32 = ctypes.c_float
+        rope = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp]
+        lib.pa_rope_and_cache.argtypes = rope + [vp, i32, i32, i32, vp, vp] + [i32] * 7 + [vp]
+        lib.pa_rope_and_cache.restype = i32
+        lib.pa_rope_and_cache_q8.argtypes = (rope + [vp, vp, i32, i32, i32, vp, vp] + [i32] * 8
+                                             + [vp])
+        lib.pa_rope_and_cache_q8.restype = i32
+        lib.pa_decode_window_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.pa_decode_window_workspace_size.restype = sz
+        lib.pa_decode_window.argtypes = ([vp, vp, vp, vp, vp, i32, vp] + [i32] * 10
+                                         + [f32, vp, sz, vp])
+        lib.pa_decode_window.restype = i32
+        lib.pa_decode_q8.argtypes = ([vp, vp, vp, vp, vp, vp, i32, vp] + [i32] * 11
+                                     + [f32, vp, sz, vp])
+        lib.pa_decode_q8.restype = i32
         lib.pa_copy_blocks.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp]
         lib.pa_copy_blocks.restype = i32
         lib.pa_status_string.argtypes = [i32]
@@ -440,6 +458,132 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, max_context
                              _ptr(query_start_loc), t, int(max_query_len), b, h, d, bs, nb,
                              float(scale), _stream(stream)),
            "pa_prefill")
+
+
+# ---- include/pa_window.h: fp16 / bf16, grouped heads, window and sinks ----
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_KV8_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _rows(t: torch.Tensor):
+    """(pointer, elements between tokens) of [tokens, heads, head_dim] rows
+    that may be a slice of a wider row."""
+    if not t.is_cuda:
+        raise ValueError("libpa takes device tensors")
+    _on_current_device(t)
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError("libpa takes token rows whose heads are contiguous")
+    return ctypes.c_void_p(t.data_ptr()), ctypes.c_int64(t.stride(0) if n > 1 else h * d)
+
+
+def _rope_args(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping):
+    """Checks and the arguments that both rotating writes share, in three parts."""
+    n, h, d = q.shape
+    nb, kvh, bs, dk = k_cache.shape
+    assert q.dtype in _DTYPES and q.dtype == q_out.dtype == key.dtype == value.dtype
+    assert q_out.shape == q.shape and key.shape == value.shape == (n, kvh, d) and dk == d
+    assert v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
+    assert slot_mapping.dtype == torch.int64 and slot_mapping.numel() == n
+    rotary = max_position = 0
+    if cos_sin is not None:
+        max_position, rotary = cos_sin.shape
+        assert cos_sin.dtype == torch.float32
+        assert positions.dtype == torch.int64 and positions.numel() == n
+    caches = [*_rows(q_out), *_rows(q), *_rows(key), *_rows(value), _ptr(k_cache), _ptr(v_cache)]
+    table = [_ptr(cos_sin), rotary, max_position]
+    rest = [_ptr(positions) if rotary else ctypes.c_void_p(None), _ptr(slot_mapping), n, h, kvh, d,
+            bs, nb, _DTYPES[q.dtype]]
+    return caches, table, rest
+
+
+def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping,
+                      interleaved=False, stream=None):
+    """Rotate q and key by their positions and write key and value at their
+    slots; q's rotated rows go to q_out (which may be q).  cos_sin
+    [max_position, rotary_dim] fp32 holds cosines, then sines (None: no
+    rotation).  q, key and value may be slices of one projection's output."""
+    assert k_cache.dtype == q.dtype
+    caches, table, rest = _rope_args(q_out, q, key, value, k_cache, v_cache, cos_sin, positions,
+                                     slot_mapping)
+    _check(load().pa_rope_and_cache(*caches, *table, int(bool(interleaved)), *rest,
+                                    _stream(stream)), "pa_rope_and_cache")
+
+
+def _check_scales(kv_scales, k_codes, v_codes):
+    nb, kvh = k_codes.shape[:2]
+    assert k_codes.dtype in _KV8_TYPES and v_codes.dtype == k_codes.dtype
+    assert v_codes.shape == k_codes.shape
+    assert kv_scales.dtype == torch.float32 and kv_scales.shape == (nb, kvh + kvh % 2, 2)
+
+
+def pa_rope_and_cache_q8(q_out, q, key, value, k_codes, v_codes, kv_scales, cos_sin, positions,
+                         slot_mapping, interleaved=False, stream=None):
+    """pa_rope_and_cache into the 8-bit cache (codes int8 or float8_e4m3fn)
+    with one scale per block and head, kv_scales [num_blocks, num_kv_heads
+    rounded up to even, 2] fp32."""
+    _check_scales(kv_scales, k_codes, v_codes)
+    caches, table, rest = _rope_args(q_out, q, key, value, k_codes, v_codes, cos_sin, positions,
+                                     slot_mapping)
+    _check(load().pa_rope_and_cache_q8(*caches, _ptr(kv_scales), *table, int(bool(interleaved)),
+                                       *rest, _KV8_TYPES[k_codes.dtype], _stream(stream)),
+           "pa_rope_and_cache_q8")
+
+
+def pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim) -> int:
+    return int(load().pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim))
+
+
+def new_window_workspace(num_seqs, num_heads, num_kv_heads, head_dim, device=None) -> torch.Tensor:
+    """Allocate (through torch) and initialise a workspace for
+    pa_decode_window and pa_decode_q8."""
+    n = pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim)
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    pa_decode_workspace_init(ws)
+    return ws
+
+
+def _context_args(out, q, k_cache, v_cache, block_tables, context_lens):
+    assert q.dtype in _DTYPES and out.dtype == q.dtype and out.shape == q.shape
+    assert v_cache.shape == k_cache.shape and k_cache.shape[3] == q.shape[2]
+    assert v_cache.dtype == k_cache.dtype
+    assert block_tables.dtype == context_lens.dtype == torch.int32 and block_tables.dim() == 2
+    assert block_tables.shape[0] == context_lens.numel()
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, window,
+                     num_sinks, scale, workspace, stream=None):
+    """One query per sequence over its paged context, seeing the last `window`
+    positions and the first `num_sinks`; grouped heads (q [B, H, D], cache
+    [blocks, KVH, block_size, D])."""
+    b, h, d = q.shape
+    nb, kvh, bs, _ = k_cache.shape
+    _context_args(out, q, k_cache, v_cache, block_tables, context_lens)
+    assert k_cache.dtype == q.dtype and context_lens.numel() == b
+    _check(load().pa_decode_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                                   int(max_context_len), int(window), int(num_sinks), b, h, kvh, d,
+                                   bs, nb, _DTYPES[q.dtype], float(scale), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+           "pa_decode_window")
+
+
+def pa_decode_q8(out, q, k_codes, v_codes, kv_scales, block_tables, context_lens, max_context_len,
+                 window, num_sinks, scale, workspace, stream=None):
+    """pa_decode_window over the 8-bit cache with one scale per block and head."""
+    b, h, d = q.shape
+    nb, kvh, bs, _ = k_codes.shape
+    _context_args(out, q, k_codes, v_codes, block_tables, context_lens)
+    _check_scales(kv_scales, k_codes, v_codes)
+    assert context_lens.numel() == b
+    _check(load().pa_decode_q8(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(kv_scales),
+                               _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                               int(max_context_len), int(window), int(num_sinks), b, h, kvh, d, bs,
+                               nb, _DTYPES[q.dtype], _KV8_TYPES[k_codes.dtype], float(scale),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(),
+                               _stream(stream)),
+           "pa_decode_q8")
 
 
 def pa_get_last_device_error() -> int:

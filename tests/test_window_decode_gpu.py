@@ -1,0 +1,160 @@
+"""One-query window attention over 16-bit and block-scaled 8-bit caches
+against the 64-bit form: masks, grouped heads, contexts split between blocks
+of threads, stale rows and given-back blocks, streams, graphs and
+workspaces."""
+import pytest
+import torch
+
+from paged_kv_cache_481_b200 import binding
+from window_helpers import Paged, check_decode, decode
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+STORES = [(F16, None), (BF16, None), (F16, "int8"), (BF16, "e4m3"), (BF16, "int8"), (F16, "e4m3")]
+
+
+@pytest.mark.parametrize("dtype,codes", STORES)
+@pytest.mark.parametrize("lens,heads,kvh,d,bs,window,sinks", [
+    ([1], 1, 1, 64, 8, 1, 0),
+    ([0, 1, 15, 16, 17, 33], 4, 4, 128, 16, 16, 0),
+    ([0, 0, 0], 4, 2, 64, 16, 5, 2),
+    ([5, 130, 64, 63, 65, 200], 14, 2, 128, 8, 50, 3),
+    ([1000, 31, 0, 999, 257], 32, 2, 64, 32, 100, 70),
+    ([300, 1, 2, 700], 17, 1, 128, 64, 1, 4),
+    ([513, 40], 128, 1, 128, 128, 300, 130),
+    ([3000, 2999], 10, 2, 128, 16, 4000, 0),
+    ([77] * 40, 6, 6, 64, 16, 20, 1000),
+])
+def test_against_64_bits(dtype, codes, lens, heads, kvh, d, bs, window, sinks):
+    paged = Paged(lens, kvh, d, bs, dtype, seed=len(lens) * 7 + d, codes=codes)
+    q = paged.randn((len(lens), heads, d))
+    out = decode(paged, q, window, sinks, d ** -0.5)
+    assert binding.pa_get_last_device_error() == 0
+    check_decode(paged, q, out, window, sinks, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,codes", STORES[:4])
+def test_long_contexts_are_split_and_merged(dtype, codes):
+    """Few units, so every unit straddles several blocks of threads; the same
+    bits on every run."""
+    paged = Paged([20011, 9, 4097], 2, 128, 16, dtype, seed=5, codes=codes)
+    q = paged.randn((3, 8, 128))
+    ws = binding.new_window_workspace(3, 8, 2, 128)
+    first = decode(paged, q, 30000, 0, 0.09, workspace=ws)
+    check_decode(paged, q, first, 30000, 0, 0.09)
+    for _ in range(5):
+        assert torch.equal(decode(paged, q, 30000, 0, 0.09, workspace=ws), first)
+
+
+@pytest.mark.parametrize("dtype,codes", STORES[:4])
+def test_blocks_that_the_window_left_are_not_looked_at(dtype, codes):
+    """Table entries of blocks without a visible position may be anything, and
+    rows that are not seen may hold NaN or infinities."""
+    lens, bs, window, sinks = [400, 97, 16], 16, 33, 3
+    paged = Paged(lens, 2, 128, bs, dtype, seed=9, codes=codes)
+    q = paged.randn((3, 4, 128))
+    want = decode(paged, q, window, sinks, 0.1)
+    check_decode(paged, q, want, window, sinks, 0.1)
+    for b, n in enumerate(lens):
+        start = n - window
+        for t in range(sinks, start):       # hidden rows
+            block = int(paged.tables[b, t // bs])
+            if codes != "int8":
+                for cache, junk in ((paged.k, float("nan")), (paged.v, float("inf"))):
+                    if codes == "e4m3":
+                        junk = float("nan")
+                    rows = cache[block, :, t % bs].float()
+                    cache[block, :, t % bs] = torch.full_like(rows, junk).to(cache.dtype)
+        for j in range(-(-sinks // bs), max(0, start) // bs):
+            paged.tables[b, j] = [-1, 2 ** 30, -7][j % 3]
+    assert torch.equal(decode(paged, q, window, sinks, 0.1), want)
+    assert binding.pa_get_last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,codes", STORES[:4])
+def test_scores_of_large_magnitude(dtype, codes):
+    """Scores up to several hundred: one token takes almost all the weight.
+    The bound's score term grows with sum |q k| scale."""
+    paged = Paged([600], 1, 64, 16, dtype, seed=13, codes=codes)
+    q = paged.randn((1, 2, 64)) * 40
+    out = decode(paged, q, 600, 0, 0.5)
+    k, v = paged.context64(0)
+    from window_helpers import attend64, attention_bound
+    ref, mass = attend64(q, k, v, [599], 600, 0, 0.5)
+    bound = attention_bound(ref, mass, dtype, F16 if codes else dtype, float(v.abs().max()), 600)
+    # (64 + 8) 2^-23 sum |q k| scale, in the weight and in the total
+    reach = torch.einsum("nhd,td->nht", q.double().abs(), k[:, 0].abs()).max() * 0.5
+    bound = bound + 2 * 72 * 2.0 ** -23 * reach * mass
+    assert bool(((out.double() - ref).abs() <= bound).all())
+
+
+def test_zero_and_negative_scale():
+    paged = Paged([100, 40], 2, 64, 16, BF16, seed=15)
+    q = paged.randn((2, 4, 64))
+    for scale in (0.0, -0.2):
+        check_decode(paged, q, decode(paged, q, 30, 2, scale), 30, 2, scale)
+
+
+def test_bad_lengths_and_blocks_are_recorded():
+    paged = Paged([50, 20], 1, 64, 8, F16, seed=3, junk=0.0)
+    q = paged.randn((2, 2, 64))
+    binding.pa_get_last_device_error()
+    decode(paged, q, 100, 0, 0.1, max_len=40)
+    assert binding.pa_get_last_device_error() == binding.PA_DEVERR_CONTEXT_LEN
+    paged.tables[1, 1] = paged.nb
+    out = decode(paged, q, 100, 0, 0.1)
+    assert binding.pa_get_last_device_error() == binding.PA_DEVERR_BLOCK_ID
+    check_decode(paged, q, out, 100, 0, 0.1, seqs=[0])
+
+
+def test_streams_graphs_and_a_shared_workspace():
+    """Calls of several sizes and types one after the other on one workspace,
+    on a side stream, and replayed from a graph."""
+    cases = [(Paged([900, 3, 2500], 2, 128, 16, BF16, seed=1), 8),
+             (Paged([5000], 1, 64, 8, F16, seed=2), 3),
+             (Paged([700, 70, 7, 0], 4, 64, 32, F16, seed=3, codes="int8"), 4),
+             (Paged([2049, 2048], 2, 128, 16, BF16, seed=4, codes="e4m3"), 64)]
+    qs = [p.randn((len(p.lens), h, p.d)) for p, h in cases]
+    size = max(binding.pa_decode_window_workspace_size(len(p.lens), h, p.kvh, p.d)
+               for p, h in cases)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    binding.pa_decode_workspace_init(ws)
+    want = [decode(p, q, 2000, 4, 0.1) for (p, _), q in zip(cases, qs)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            got = [decode(p, q, 2000, 4, 0.1, workspace=ws) for (p, _), q in zip(cases, qs)]
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    tables = [p.dev_tables() for p, _ in cases]
+    outs = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for (p, _), q, (t, n), o in zip(cases, qs, tables, outs):
+            if p.codes:
+                binding.pa_decode_q8(o, q, p.k, p.v, p.scales, t, n, max(p.lens), 2000, 4, 0.1, ws)
+            else:
+                binding.pa_decode_window(o, q, p.k, p.v, t, n, max(p.lens), 2000, 4, 0.1, ws)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+
+
+def test_whole_context_agrees_with_pa_decode():
+    """fp16, one query head per K/V head and a window over everything is
+    pa_decode's case; both are within their bounds of the same sum."""
+    paged = Paged([1, 40, 700, 2000], 8, 128, 16, F16, seed=8)
+    q = paged.randn((4, 8, 128))
+    out, old = decode(paged, q, 2000, 0, 0.1), torch.empty_like(q)
+    tables, lens = paged.dev_tables()
+    binding.pa_decode(old, q, paged.k, paged.v, tables, lens, 2000, 0.1,
+                      binding.new_workspace(4, 8, 128, 2000))
+    check_decode(paged, q, out, 2000, 0, 0.1)
+    check_decode(paged, q, old, 2000, 0, 0.1)
