@@ -157,6 +157,29 @@ PA_API pa_status pa_decode_q8(void *out, const void *q, const void *k_codes, con
                               int num_blocks, pa_dtype dtype, pa_kv8_type kv_type, float scale,
                               void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
+/*
+ * The same attention for several queries a sequence (prompts, chunks that
+ * continue a cached context, draft tokens): the last n_b =
+ * query_start_loc[b+1] - query_start_loc[b] of sequence b's context_lens[b]
+ * cached tokens are its queries, at positions L - n_b + i, as in pa_prefill.
+ * Runs on the tensor cores (tcgen05); scores and sums fp32, the weights enter
+ * the product with V in the cache's 16-bit type.  scale must be finite and
+ * > 0.  Rows of q and out that belong to no sequence are left as they are.
+ * A V row that is not finite may reach queries of its sequence that are less
+ * than 256 positions away even where the mask hides it from them; rows that
+ * no such query sees have no effect.  n_b > L_b or > max_query_len,
+ * or rows outside q, are recorded (PA_DEVERR_CONTEXT_LEN) and that sequence
+ * is skipped.
+ */
+PA_API pa_status pa_prefill_window(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *context_lens,
+                                   int max_context_len, const int32_t *query_start_loc,
+                                   int num_tokens, int max_query_len, int window, int num_sinks,
+                                   int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int num_blocks, pa_dtype dtype, float scale,
+                                   pa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

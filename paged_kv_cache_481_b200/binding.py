@@ -39,7 +39,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_works
             "pa_bm_swap_in", "pa_decode_append", "pa_decode_grouped_workspace_size",
             "pa_decode_grouped", "pa_decode_contiguous", "pa_rope_and_cache",
             "pa_rope_and_cache_q8", "pa_decode_window_workspace_size", "pa_decode_window",
-            "pa_decode_q8")
+            "pa_decode_q8", "pa_prefill_window")
 
 _lock = threading.Lock()
 _lib = None
@@ -149,6 +149,9 @@ def load(path: str | None = None):
         lib.pa_decode_q8.argtypes = ([vp, vp, vp, vp, vp, vp, i32, vp] + [i32] * 11
                                      + [f32, vp, sz, vp])
         lib.pa_decode_q8.restype = i32
+        lib.pa_prefill_window.argtypes = ([vp, vp, vp, vp, vp, i32, vp, i32, vp] + [i32] * 11
+                                          + [f32, vp])
+        lib.pa_prefill_window.restype = i32
         lib.pa_copy_blocks.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp]
         lib.pa_copy_blocks.restype = i32
         lib.pa_status_string.argtypes = [i32]
@@ -583,7 +586,25 @@ def pa_decode_q8(out, q, k_codes, v_codes, kv_scales, block_tables, context_lens
                                nb, _DTYPES[q.dtype], _KV8_TYPES[k_codes.dtype], float(scale),
                                _ptr(workspace), workspace.numel() * workspace.element_size(),
                                _stream(stream)),
-           "pa_decode_q8")
+           "pa_decode_q8", "pa_prefill_window")
+
+
+def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                      query_start_loc, max_query_len, window, num_sinks, scale, stream=None):
+    """pa_prefill with grouped heads, fp16 or bf16, and the visibility rule of
+    pa_decode_window at each query's position."""
+    t, h, d = q.shape
+    nb, kvh, bs, _ = k_cache.shape
+    _context_args(out, q, k_cache, v_cache, block_tables, context_lens)
+    b = context_lens.numel()
+    assert k_cache.dtype == q.dtype
+    assert query_start_loc.dtype == torch.int32 and query_start_loc.numel() == b + 1
+    _check(load().pa_prefill_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                                    int(max_context_len), _ptr(query_start_loc), t,
+                                    int(max_query_len), int(window), int(num_sinks), b, h, kvh, d,
+                                    bs, nb, _DTYPES[q.dtype], float(scale), _stream(stream)),
+           "pa_prefill_window")
 
 
 def pa_get_last_device_error() -> int:

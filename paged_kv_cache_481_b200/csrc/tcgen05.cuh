@@ -177,6 +177,12 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32_mn(int m, int n, bool a_mn_
     return idesc_f16_f32(m, n, b_mn_major) | (uint32_t(a_mn_major) << 15);
 }
 
+// The same for fp16 or bf16 operands (one type for both), A K-major.
+__host__ __device__ constexpr uint32_t idesc_16_f32(int m, int n, bool b_mn_major, bool bf16)
+{
+    return idesc_f16_f32(m, n, b_mn_major) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10);
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by a single thread.
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate)
@@ -220,6 +226,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Box of a 3-D tensor map at (x0, x1, x2); x0 times the element size must be a
+// multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x0, int x1, int x2,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x0), "r"(x1), "r"(x2)
         : "memory");
 }
 

@@ -86,3 +86,26 @@ def test_workspace_size(lib):
     assert size(8, 32, 8, 64) == size(8, 32, 8, 128)
     # a counter per (sequence, K/V head, 16 query heads)
     assert size(1000, 32, 1, 64) - size(0, 1, 1, 64) >= 2 * 1000 * 4 - 256
+
+
+def _prefill(lib, **change):
+    a = dict(out=P, q=P, k=P, v=P, tables=P, mb=4, lens=P, maxlen=64, starts=P, n=8, maxnew=8,
+             window=16, sinks=0, b=1, h=4, kvh=2, d=64, bs=16, nb=4, dtype=0, scale=1.0, stream=NULL)
+    a.update(change)
+    return lib.pa_prefill_window(*a.values())
+
+
+def test_prefill_refuses(lib):
+    r = lambda **c: _prefill(lib, **c)
+    for c in (dict(b=0), dict(n=0), dict(maxnew=0)):
+        assert r(q=NULL, **c) == OK
+    for c in (dict(b=-1), dict(b=70000), dict(n=-1), dict(maxnew=-1), dict(nb=0), dict(maxlen=-1),
+              dict(mb=-1), dict(window=0), dict(sinks=-1), dict(dtype=2), dict(h=5),
+              dict(h=512, kvh=2), dict(scale=float("nan")), dict(scale=0.0), dict(scale=-1.0),
+              dict(maxlen=65), dict(maxnew=65), dict(maxlen=2 ** 30 + 1, mb=2 ** 30),
+              dict(nb=2 ** 30), dict(out=NULL), dict(q=NULL), dict(k=NULL), dict(v=NULL),
+              dict(tables=NULL), dict(lens=NULL), dict(starts=NULL), dict(out=ODD), dict(q=ODD),
+              dict(k=ODD), dict(starts=ctypes.c_void_p(0x10002))):
+        assert r(**c) == INVALID, c
+    for c in (dict(d=96), dict(bs=12), dict(d=256)):
+        assert r(**c) == UNSUPPORTED, c
