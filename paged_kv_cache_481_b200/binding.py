@@ -464,41 +464,64 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, max_context
 
 
 # ---- include/pa_window.h: fp16 / bf16, grouped heads, window and sinks ----
+# A step's smallest calls take the GPU a few microseconds, so these wrappers
+# keep the host's part short: one look at the current device and stream a
+# call, pointers and sizes as plain integers (argtypes convert them).
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _KV8_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 
-def _rows(t: torch.Tensor):
-    """(pointer, elements between tokens) of [tokens, heads, head_dim] rows
-    that may be a slice of a wider row."""
-    if not t.is_cuda:
-        raise ValueError("libpa takes device tensors")
-    _on_current_device(t)
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError("libpa takes token rows whose heads are contiguous")
-    return ctypes.c_void_p(t.data_ptr()), ctypes.c_int64(t.stride(0) if n > 1 else h * d)
+def _raw_stream(stream) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _rope_args(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping):
-    """Checks and the arguments that both rotating writes share, in three parts."""
+def _pointers(device: int, *tensors):
+    """Addresses of contiguous tensors on the current device."""
+    for t in tensors:
+        if t.get_device() != device or not t.is_contiguous():
+            _ptr(t)   # says what is wrong
+    return [t.data_ptr() for t in tensors]
+
+
+def _rows(device: int, *tensors):
+    """Addresses and elements between tokens of [tokens, heads, head_dim] rows
+    that may be slices of wider rows."""
+    out = []
+    for t in tensors:
+        n, h, d = t.shape
+        if t.get_device() != device:
+            _ptr(t)
+        step, head, one = t.stride()
+        if (d > 1 and one != 1) or (h > 1 and head != d):
+            raise ValueError("libpa takes token rows whose heads are contiguous")
+        out += (t.data_ptr(), step if n > 1 else h * d)
+    return out
+
+
+def _rope_args(q_out, q, key, value, k_cache, v_cache, scales, cos_sin, positions, slot_mapping,
+               interleaved):
+    """Checks and the arguments that both rotating writes share."""
     n, h, d = q.shape
     nb, kvh, bs, dk = k_cache.shape
-    assert q.dtype in _DTYPES and q.dtype == q_out.dtype == key.dtype == value.dtype
+    dtype = q.dtype
+    assert dtype in _DTYPES and dtype == q_out.dtype == key.dtype == value.dtype
     assert q_out.shape == q.shape and key.shape == value.shape == (n, kvh, d) and dk == d
     assert v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
     assert slot_mapping.dtype == torch.int64 and slot_mapping.numel() == n
-    rotary = max_position = 0
-    if cos_sin is not None:
+    device = torch.cuda.current_device()
+    if cos_sin is None:
+        table = [0, 0, 0, int(interleaved), 0]
+    else:
         max_position, rotary = cos_sin.shape
         assert cos_sin.dtype == torch.float32
         assert positions.dtype == torch.int64 and positions.numel() == n
-    caches = [*_rows(q_out), *_rows(q), *_rows(key), *_rows(value), _ptr(k_cache), _ptr(v_cache)]
-    table = [_ptr(cos_sin), rotary, max_position]
-    rest = [_ptr(positions) if rotary else ctypes.c_void_p(None), _ptr(slot_mapping), n, h, kvh, d,
-            bs, nb, _DTYPES[q.dtype]]
-    return caches, table, rest
+        cos_sin, positions = _pointers(device, cos_sin, positions)
+        table = [cos_sin, rotary, max_position, int(interleaved), positions if rotary else 0]
+    return [*_rows(device, q_out, q, key, value), *_pointers(device, k_cache, v_cache, *scales), *table,
+            *_pointers(device, slot_mapping), n, h, kvh, d, bs, nb, _DTYPES[dtype]]
 
 
 def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping,
@@ -508,10 +531,9 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, cos_sin, positions
     [max_position, rotary_dim] fp32 holds cosines, then sines (None: no
     rotation).  q, key and value may be slices of one projection's output."""
     assert k_cache.dtype == q.dtype
-    caches, table, rest = _rope_args(q_out, q, key, value, k_cache, v_cache, cos_sin, positions,
-                                     slot_mapping)
-    _check(load().pa_rope_and_cache(*caches, *table, int(bool(interleaved)), *rest,
-                                    _stream(stream)), "pa_rope_and_cache")
+    args = _rope_args(q_out, q, key, value, k_cache, v_cache, (), cos_sin, positions, slot_mapping,
+                      interleaved)
+    _check((_lib or load()).pa_rope_and_cache(*args, _raw_stream(stream)), "pa_rope_and_cache")
 
 
 def _check_scales(kv_scales, k_codes, v_codes):
@@ -527,11 +549,10 @@ def pa_rope_and_cache_q8(q_out, q, key, value, k_codes, v_codes, kv_scales, cos_
     with one scale per block and head, kv_scales [num_blocks, num_kv_heads
     rounded up to even, 2] fp32."""
     _check_scales(kv_scales, k_codes, v_codes)
-    caches, table, rest = _rope_args(q_out, q, key, value, k_codes, v_codes, cos_sin, positions,
-                                     slot_mapping)
-    _check(load().pa_rope_and_cache_q8(*caches, _ptr(kv_scales), *table, int(bool(interleaved)),
-                                       *rest, _KV8_TYPES[k_codes.dtype], _stream(stream)),
-           "pa_rope_and_cache_q8")
+    args = _rope_args(q_out, q, key, value, k_codes, v_codes, (kv_scales,), cos_sin, positions,
+                      slot_mapping, interleaved)
+    _check((_lib or load()).pa_rope_and_cache_q8(*args, _KV8_TYPES[k_codes.dtype],
+                                                 _raw_stream(stream)), "pa_rope_and_cache_q8")
 
 
 def pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim) -> int:
@@ -547,12 +568,28 @@ def new_window_workspace(num_seqs, num_heads, num_kv_heads, head_dim, device=Non
     return ws
 
 
-def _context_args(out, q, k_cache, v_cache, block_tables, context_lens):
+def _context_args(out, q, k_cache, v_cache, scales, block_tables, context_lens, max_context_len):
+    """Checks and leading arguments that the window attentions share."""
     assert q.dtype in _DTYPES and out.dtype == q.dtype and out.shape == q.shape
     assert v_cache.shape == k_cache.shape and k_cache.shape[3] == q.shape[2]
     assert v_cache.dtype == k_cache.dtype
-    assert block_tables.dtype == context_lens.dtype == torch.int32 and block_tables.dim() == 2
-    assert block_tables.shape[0] == context_lens.numel()
+    assert block_tables.dtype == context_lens.dtype == torch.int32
+    rows, width = block_tables.shape
+    assert rows == context_lens.numel()
+    *caches, tables, lens = _pointers(torch.cuda.current_device(), out, q, k_cache, v_cache, *scales,
+                                      block_tables, context_lens)
+    return [*caches, tables, width, lens, int(max_context_len)]
+
+
+def _decode_args(out, q, k_cache, v_cache, scales, kinds, block_tables, context_lens,
+                 max_context_len, window, num_sinks, scale, workspace, stream):
+    b, h, d = q.shape
+    nb, kvh, bs, _ = k_cache.shape
+    assert context_lens.numel() == b
+    return (*_context_args(out, q, k_cache, v_cache, scales, block_tables, context_lens,
+                           max_context_len), int(window), int(num_sinks), b, h, kvh, d, bs, nb, *kinds,
+            float(scale), *_pointers(torch.cuda.current_device(), workspace),
+            workspace.numel() * workspace.element_size(), _raw_stream(stream))
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, window,
@@ -560,33 +597,20 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, max_c
     """One query per sequence over its paged context, seeing the last `window`
     positions and the first `num_sinks`; grouped heads (q [B, H, D], cache
     [blocks, KVH, block_size, D])."""
-    b, h, d = q.shape
-    nb, kvh, bs, _ = k_cache.shape
-    _context_args(out, q, k_cache, v_cache, block_tables, context_lens)
-    assert k_cache.dtype == q.dtype and context_lens.numel() == b
-    _check(load().pa_decode_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                                   int(max_context_len), int(window), int(num_sinks), b, h, kvh, d,
-                                   bs, nb, _DTYPES[q.dtype], float(scale), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)),
-           "pa_decode_window")
+    assert k_cache.dtype == q.dtype
+    args = _decode_args(out, q, k_cache, v_cache, (), (_DTYPES[q.dtype],), block_tables, context_lens,
+                        max_context_len, window, num_sinks, scale, workspace, stream)
+    _check((_lib or load()).pa_decode_window(*args), "pa_decode_window")
 
 
 def pa_decode_q8(out, q, k_codes, v_codes, kv_scales, block_tables, context_lens, max_context_len,
                  window, num_sinks, scale, workspace, stream=None):
     """pa_decode_window over the 8-bit cache with one scale per block and head."""
-    b, h, d = q.shape
-    nb, kvh, bs, _ = k_codes.shape
-    _context_args(out, q, k_codes, v_codes, block_tables, context_lens)
     _check_scales(kv_scales, k_codes, v_codes)
-    assert context_lens.numel() == b
-    _check(load().pa_decode_q8(_ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(kv_scales),
-                               _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                               int(max_context_len), int(window), int(num_sinks), b, h, kvh, d, bs,
-                               nb, _DTYPES[q.dtype], _KV8_TYPES[k_codes.dtype], float(scale),
-                               _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream(stream)),
-           "pa_decode_q8", "pa_prefill_window")
+    args = _decode_args(out, q, k_codes, v_codes, (kv_scales,),
+                        (_DTYPES[q.dtype], _KV8_TYPES[k_codes.dtype]), block_tables, context_lens,
+                        max_context_len, window, num_sinks, scale, workspace, stream)
+    _check((_lib or load()).pa_decode_q8(*args), "pa_decode_q8")
 
 
 def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
@@ -595,16 +619,14 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, max_
     pa_decode_window at each query's position."""
     t, h, d = q.shape
     nb, kvh, bs, _ = k_cache.shape
-    _context_args(out, q, k_cache, v_cache, block_tables, context_lens)
     b = context_lens.numel()
     assert k_cache.dtype == q.dtype
     assert query_start_loc.dtype == torch.int32 and query_start_loc.numel() == b + 1
-    _check(load().pa_prefill_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                                    int(max_context_len), _ptr(query_start_loc), t,
-                                    int(max_query_len), int(window), int(num_sinks), b, h, kvh, d,
-                                    bs, nb, _DTYPES[q.dtype], float(scale), _stream(stream)),
-           "pa_prefill_window")
+    args = _context_args(out, q, k_cache, v_cache, (), block_tables, context_lens, max_context_len)
+    _check((_lib or load()).pa_prefill_window(
+        *args, *_pointers(torch.cuda.current_device(), query_start_loc), t, int(max_query_len),
+        int(window), int(num_sinks), b, h, kvh, d, bs, nb, _DTYPES[q.dtype], float(scale),
+        _raw_stream(stream)), "pa_prefill_window")
 
 
 def pa_get_last_device_error() -> int:
