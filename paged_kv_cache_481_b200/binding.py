@@ -474,7 +474,7 @@ _KV8_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 def _raw_stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

@@ -4,6 +4,7 @@
 // window_decode_kernel.cuh.  Nothing here allocates device memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -12,38 +13,42 @@
 #include "host_common.cuh"
 #include "window_decode_kernel.cuh"
 #include "window_host.cuh"
+#include "window_maps.cuh"
 
 namespace {
 
-// Two partial-result slots per CTA (its first and its last unit, the only
-// ones that can straddle CTAs), then one merge counter per unit.  The slots
-// have room for head_dim 128 whatever the call's is, so that the counters of
-// calls that share a workspace always lie in the same place.
+// Two partial-result slots per range (its first and its last unit, the only
+// ones that can straddle ranges), then one merge counter per unit.  The slots
+// have room for the most any call needs, so that the counters of calls that
+// share a workspace always lie in the same place.
 struct WindowWorkspace {
     size_t ml_off, ticket_off, total;
 };
 
-int row_tiles(int num_heads, int num_kv_heads)
+// query heads of a unit: 8, or 16 for larger groups
+int unit_heads(int group)
 {
-    return (num_heads / num_kv_heads + 15) / 16;
+    return group <= 8 ? 8 : 16;
 }
 
 WindowWorkspace window_workspace(int num_seqs, int num_heads, int num_kv_heads)
 {
     WindowWorkspace w{};
-    const size_t slots = size_t(pa::kWdMaxCtas) * 2;
-    const size_t units = size_t(num_seqs) * num_kv_heads * row_tiles(num_heads, num_kv_heads);
+    const int group = num_heads / num_kv_heads, per = unit_heads(group);
+    const size_t slots = size_t(pa::kWdMaxRanges) * 2;
+    const size_t units = size_t(num_seqs) * num_kv_heads * ((group + per - 1) / per);
     w.ml_off = align256(slots * 16 * 128 * sizeof(float));
     w.ticket_off = w.ml_off + align256(slots * 16 * sizeof(float2));
     w.total = w.ticket_off + align256((units > 0 ? units : 1) * sizeof(unsigned));
     return w;
 }
 
-template <pa::KvStore kStore, int D>
-pa_status launch_window(const pa::WindowDecodeParams &p, cudaStream_t stream)
+template <pa::KvStore kStore, int D, int kNq>
+pa_status launch_window(const pa::WindowDecodeParams &p, const void *k, const void *v,
+                        cudaStream_t stream)
 {
     using W = pa::WindowTraits<kStore, D>;
-    constexpr auto kernel = pa::window_decode_kernel<kStore, D>;
+    constexpr auto kernel = pa::window_decode_kernel<kStore, D, kNq>;
     static std::atomic<int> grid_for[kMaxDevices];  // 0 = not configured yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -57,13 +62,21 @@ pa_status launch_window(const pa::WindowDecodeParams &p, cudaStream_t stream)
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, pa::kWdThreads,
                                                           W::kSmem) != cudaSuccess)
             return PA_ERR_CUDA;
-        grid = sms * (per_sm > 0 ? per_sm : 1);
-        if (grid > pa::kWdMaxCtas)
-            grid = pa::kWdMaxCtas;
+        grid = std::min(sms * std::max(per_sm, 1), pa::kWdMaxCtas);
         grid_for[dev].store(grid, std::memory_order_release);
     }
-    return launch_pdl(kernel, dim3(unsigned(grid)), dim3(pa::kWdThreads), W::kSmem, stream, p) ==
-                   cudaSuccess
+    CUtensorMap tm_k, tm_v;
+    const uint64_t rows = (uint64_t(p.num_blocks) * p.kv_heads) << p.log2_bs;
+    const uint32_t box = uint32_t(std::min(1 << p.log2_bs, W::kTile));
+    const bool ok = [&] {
+        if constexpr (W::kEight)
+            return line_map(&tm_k, k, rows * D / 128, box * D / 128) &&
+                   line_map(&tm_v, v, rows * D / 128, box * D / 128);
+        else
+            return cache_map<D>(&tm_k, k, rows, box) && cache_map<D>(&tm_v, v, rows, box);
+    }();
+    return ok && launch_pdl(kernel, dim3(unsigned(grid)), dim3(pa::kWdThreads), W::kSmem, stream, tm_k,
+                            tm_v, p) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
@@ -98,11 +111,17 @@ pa_status window_decode(void *out, const void *q, const void *k, const void *v,
     if (!aligned16(workspace))
         return PA_ERR_INVALID_ARG;
 
+    // the tensor maps address the caches in groups of 8 rows or lines of 128
+    // bytes; the work is counted in 64 bits
+    const int64_t cache_bytes = int64_t(num_blocks) * num_kv_heads * block_size * head_dim *
+                                (eight ? 1 : 2);
+    if (cache_bytes / (eight ? 128 : 16 * head_dim) > INT32_MAX ||
+        int64_t(num_seqs) * num_heads * (max_context_len / 16 + 1) > (int64_t(1) << 50))
+        return PA_ERR_INVALID_ARG;
+
     pa::WindowDecodeParams p{};
     p.out = out;
     p.q = q;
-    p.k = k;
-    p.v = v;
     p.scales = reinterpret_cast<const float2 *>(scales);
     p.tables = block_tables;
     p.lens = context_lens;
@@ -114,28 +133,30 @@ pa_status window_decode(void *out, const void *q, const void *k, const void *v,
     p.heads = num_heads;
     p.kv_heads = num_kv_heads;
     p.group = num_heads / num_kv_heads;
-    p.row_tiles = row_tiles(num_heads, num_kv_heads);
+    const int per = unit_heads(p.group);
+    p.row_tiles = (p.group + per - 1) / per;
     p.log2_bs = __builtin_ctz(unsigned(block_size));
     p.num_blocks = num_blocks;
     p.scale_heads = scale_heads(num_kv_heads);
     p.bf16 = dtype == PA_BF16;
     p.scale_log2 = float(double(scale) * 1.4426950408889634);
-    p.min_tiles = 8;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    p.part_o = reinterpret_cast<float *>(ws);
-    p.part_ml = reinterpret_cast<float2 *>(ws + w.ml_off);
+    p.part_o = reinterpret_cast<float4 *>(ws);
+    p.part_ml = reinterpret_cast<float4 *>(ws + w.ml_off);
     p.tickets = reinterpret_cast<unsigned *>(ws + w.ticket_off);
     p.err = device_error_word();
     if (!p.err)
         return PA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_bool(head_dim == 128, [&](auto d128) {
-        constexpr int D = d128 ? 128 : 64;
-        if (eight)
-            return kv_type == PA_KV8_E4M3 ? launch_window<pa::KvStore::kE4m3, D>(p, st)
-                                          : launch_window<pa::KvStore::kInt8, D>(p, st);
-        return dtype == PA_BF16 ? launch_window<pa::KvStore::kBf16, D>(p, st)
-                                : launch_window<pa::KvStore::kF16, D>(p, st);
+        return with_bool(per == 16, [&](auto many) {
+            constexpr int D = d128 ? 128 : 64, kNq = many ? 2 : 1;
+            if (eight)
+                return kv_type == PA_KV8_E4M3 ? launch_window<pa::KvStore::kE4m3, D, kNq>(p, k, v, st)
+                                              : launch_window<pa::KvStore::kInt8, D, kNq>(p, k, v, st);
+            return dtype == PA_BF16 ? launch_window<pa::KvStore::kBf16, D, kNq>(p, k, v, st)
+                                    : launch_window<pa::KvStore::kF16, D, kNq>(p, k, v, st);
+        });
     });
 }
 

@@ -4,44 +4,55 @@
 //
 // Mathematics: the query at p = L - 1 sees t < L with t >= ws = max(0, L -
 // window) or t < sinks; out = sum_t w_t V_t / sum_t w_t with w_t =
-// 2^(c s_t - m), taken in one pass over the visible tokens with the running
-// maximum m (online softmax in base 2).
+// 2^(c s_t - m), taken in one pass over the visible tokens.  The reference m
+// is moved only when a score passes it by more than 2^8, so most tiles need
+// one vote and no reduction; numerator and denominator always share it.
 //
-// What bounds it: reading K and V once, 4 D bytes a token and K/V head for
-// about 4 D flops a query head and token, so memory as long as the matrix
-// work is not done on scalar units.  The G query heads of a K/V head are the
-// rows of a 16-row warp matrix product, so K and V are read once per group
-// and a tile costs the same few instructions for any G <= 16.
+// What bounds it: reading K and V once, 4 D bytes a token and K/V head (2 D
+// in 8 bits) for about 4 D flops a query head and token, so memory as long as
+// a tile costs few instructions.  Both products are warp matrix products with
+// the tokens (K Q^T) or the dims (V^T P^T) as their 16 rows and the query
+// heads of the K/V head as their 8 columns: for up to 8 heads that is half the
+// products, sums and accumulators of the other order, and K and V are read
+// once per group.  (tcgen05 needs 64 rows and more and its operands through
+// one more hop; at these sizes the copies would wait for it.)
 //
-// Layout of the work: a "unit" is (sequence, K/V head, 16 query heads); its
-// visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens at
-// D = 128 in 16 bits).  The tiles of all units, unit after unit, are cut into
-// equal contiguous ranges, one per CTA; within a range the tiles of a unit go
-// to the CTA's warps in turn.  Each warp has its own ring of kStages tiles,
-// filled by 16-byte asynchronous copies (rows that are not seen are written
-// as zeros and not read) and keeps it full across units.  Rows of 128 bytes
-// and more are XOR-swizzled in shared memory, so matrix loads have no bank
-// conflicts.  The warps' results of a unit are merged in shared memory; a
-// unit that straddles CTAs leaves partial results in the workspace, and the
-// last CTA to arrive merges them in CTA order, so that the result does not
-// depend on the order of arrival.
+// Layout of the work: a "unit" is (sequence, K/V head, 8 * kNq query heads);
+// its visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens
+// at D = 128 in 16 bits).  The tiles of all units, unit after unit, are cut
+// into equal contiguous ranges.  A range belongs to a warp, which then needs
+// nobody else until the end of a unit that straddles ranges, or, when there
+// are so few units that each would be cut into more than 8 parts, to the four
+// warps of a CTA, which take its tiles in turn and merge in shared memory.
+// Cuts within 2 tiles of a unit's end move there.  A straddling unit's parts
+// go to the workspace and the last range to arrive merges them in order, so
+// the result does not depend on the order of arrival.
 //
-// Choices of fewer bits: the weights enter the product with V in 16 bits.
-// They are taken 2^14 times larger than the softmax's (numerator and
-// denominator alike), which keeps weights down to 2^-38 of the largest in
-// fp16 instead of losing those under 2^-24.  With 8-bit codes the products
-// are fp16 (codes are exact in it): the query row is scaled by a power of two
-// so that its largest component is near 2^14, exact for every component above
-// 2^-28 of it; a block's s_v is folded into its weights relative to a running
-// power of two at or above the largest s_v so far.
+// Each warp keeps a ring of kStages tiles full, across units: one lane per
+// block run issues TMA boxes (K and V) that complete an mbarrier, with the
+// 128-byte swizzle that keeps matrix loads free of bank conflicts.  The block
+// ids of the next tile are looked up one tile ahead.  Rows of a loaded run
+// that the mask hides are zeroed in V and masked in the scores.  Waits are
+// bounded; one that runs out records PA_DEVERR_TIMEOUT.
+//
+// Choices of fewer bits: the weights enter the product with V in 16 bits,
+// 2^7 times larger than the softmax's (numerator and denominator alike;
+// below 2^15 with the stale reference), which keeps weights down to 2^-31 of
+// the largest in fp16.  With 8-bit codes the products are fp16 (codes are
+// exact in it): the query row is scaled by a power of two so that its largest
+// component is near 2^14, exact for every component above 2^-28 of it; a
+// block's s_v is folded into its weights relative to a running power of two
+// at or above the largest s_v so far.
 #pragma once
 
+#include <cuda.h>
 #include <cstdint>
 
 #include "../../include/pa_window.h"
 #include "half_types.cuh"
 #include "mma_sync.cuh"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace pa {
 
@@ -50,18 +61,16 @@ enum class KvStore { kF16, kBf16, kInt8, kE4m3 };
 struct WindowDecodeParams {
     void *out;                  // [B, H, D]
     const void *q;              // [B, H, D]
-    const void *k, *v;          // caches or codes [NB, KVH, bs, D]
     const float2 *scales;       // [NB, scale_heads] (8-bit)
     const int32_t *tables;      // [B, max_blocks]
     const int32_t *lens;        // [B]
     int max_blocks, max_len, window, sinks;
-    int num_seqs, heads, kv_heads, group, row_tiles;  // row_tiles = ceil(group / 16)
+    int num_seqs, heads, kv_heads, group, row_tiles;  // row_tiles = ceil(group / (8 kNq))
     int log2_bs, num_blocks, scale_heads;
     int bf16;                   // type of q and out
     float scale_log2;           // softmax scale * log2(e)
-    int min_tiles;              // least tiles per CTA
-    float *part_o;              // [2 * CTAs, 16, D]
-    float2 *part_ml;            // [2 * CTAs, 16] (m, l)
+    float4 *part_o;             // [2 * ranges][kNq][D / 16][32 lanes]
+    float4 *part_ml;            // [2 * ranges][kNq][4] (m, l) of two query heads
     unsigned *tickets;          // [units]
     unsigned *err;
 };
@@ -69,35 +78,54 @@ struct WindowDecodeParams {
 constexpr int kWdWarps = 4;
 constexpr int kWdThreads = kWdWarps * 32;
 constexpr int kWdMaxCtas = 512;
-constexpr float kWdShift = 14.0f;   // weights are 2^14 times the softmax's
+constexpr int kWdMaxRanges = kWdMaxCtas * kWdWarps;
+constexpr float kWdShift = 7.0f;     // weights are 2^7 times the softmax's
+constexpr float kWdRescale = 8.0f;   // move the reference only past this growth
+// Least tiles of a range: a part of a unit costs about as much as 2 tiles
+// (its write, the counter, its share of the merge).
+constexpr int kWdMinTilesWarp = 4, kWdMinTilesTeam = 8;
+constexpr int kWdSnap = 2;           // cuts this close to a unit's end move there
+constexpr int kWdMaxParts = 8;       // parts a unit may have on average with warp ranges
 
 template <KvStore kStore, int D>
 struct WindowTraits {
     static constexpr bool kEight = kStore == KvStore::kInt8 || kStore == KvStore::kE4m3;
     static constexpr bool kBf16 = kStore == KvStore::kBf16;
-    static constexpr int kStages = 3;
+    static constexpr int kStages = 2;
     static constexpr int kRowBytes = D * (kEight ? 1 : 2);
     static constexpr int kTile = 4096 / kRowBytes;        // tokens per tile
-    static constexpr int kGroups = kTile / 8;             // 8-token groups: one block each
-    static constexpr int kChunks = kRowBytes / 16;        // 16-byte chunks per row
-    static constexpr int kRowsPerCopy = 32 / kChunks;     // rows one warp-wide copy covers
-    static constexpr int kScaleBytes = kEight ? kGroups * 8 : 0;
+    static constexpr int kMt = kTile / 16;                // 16-token rows of products per tile
     static constexpr int kStageBytes = 8192;
-    static constexpr int kPitch = 64 + 8;                 // merge rows of 64 dims, no bank conflicts
     static constexpr int kOffMerge = kWdWarps * kStages * kStageBytes;
-    static constexpr int kOffMl = kOffMerge + kWdWarps * 8 * kPitch * 4;
-    static constexpr int kOffScales = kOffMl + kWdWarps * 16 * 8;
-    static constexpr int kSmem = kOffScales + kWdWarps * kStages * kScaleBytes;
+    static constexpr int kOffMl = kOffMerge + kWdWarps * 4 * 32 * 16;  // 4 fragments a warp
+    static constexpr int kSmem = kOffMl + kWdWarps * 8 * 8;
 
-    // Byte offset of a 16-byte chunk of a row in a swizzled tile.
-    static __device__ __forceinline__ uint32_t at(int row, int chunk)
+    // Byte offset of a 16-byte chunk of a token's row in a tile: 128-byte
+    // lines, the chunk's place XORed with the line's number mod 8.
+    static __device__ __forceinline__ uint32_t at(int token, int chunk)
     {
-        if constexpr (kRowBytes >= 128) {
-            return uint32_t(row * kRowBytes + ((chunk ^ (row & 7)) << 4));
-        } else {  // two 64-byte rows share a 128-byte line
-            const int line = row >> 1;
-            return uint32_t(line * 128 + (((((row & 1) << 2) | chunk) ^ ((line & 3) << 1)) << 4));
+        if constexpr (!kEight) {          // [8-token group][64-dim half][8 tokens]
+            const int r = token & 7;
+            return uint32_t(((token >> 3) * (D / 64) + (chunk >> 3)) * 1024 + r * 128 +
+                            (((chunk & 7) ^ r) << 4));
+        } else if constexpr (D == 128) {  // a token a line
+            return uint32_t(token * 128 + ((chunk ^ (token & 7)) << 4));
+        } else {                          // two tokens a line
+            const int line = token >> 1;
+            return uint32_t(line * 128 + (((((token & 1) << 2) | chunk) ^ (line & 7)) << 4));
         }
+    }
+
+    // Token of product row g (+ 8 when `high`) within 16 tokens: an order in
+    // which the 8-bit rows' loads have no bank conflicts.
+    static __device__ __forceinline__ int token_of(int g, int high)
+    {
+        if constexpr (!kEight)
+            return g + 8 * high;
+        else if constexpr (D == 128)
+            return ((g & 1) ? (g - 1) ^ 5 : g) + 8 * high;
+        else
+            return 4 * (g >> 1) + (g & 1) + 2 * high;
     }
 };
 
@@ -127,11 +155,12 @@ struct WindowView {
     }
 };
 
-// A stretch [i, end) of one unit's tiles that belongs to this CTA, and what
-// of the CTA's range is left behind it.
+// A stretch [begin, end) of one unit's tiles that belongs to this range, and
+// how much of the range is left behind it.
 struct WindowSegment {
     int b, r;              // sequence, unit within the sequence
     int begin, end;
+    long long u0;          // number of the unit's first tile in the list
     long long left;
     WindowView view;
 
@@ -140,6 +169,7 @@ struct WindowSegment {
     {
         if (left <= 0)
             return false;
+        u0 += view.tiles;
         if (++r == units) {
             r = 0;
             do {
@@ -183,30 +213,37 @@ __device__ __forceinline__ float pow2_at_least(float x)
     return __uint_as_float((__float_as_uint(x) + 0x7fffffu) & 0x7f800000u);
 }
 
-template <KvStore kStore, int D>
-__global__ void __launch_bounds__(kWdThreads, 2) window_decode_kernel(const WindowDecodeParams p)
+
+template <KvStore kStore, int D, int kNq>
+__global__ void __launch_bounds__(kWdThreads, 3)
+    window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ WindowDecodeParams p)
 {
     using W = WindowTraits<kStore, D>;
-    constexpr int kTile = W::kTile, kNT = W::kGroups, kStages = W::kStages;
+    constexpr int kTile = W::kTile, kMt = W::kMt, kStages = W::kStages, kDt = D / 16;
     constexpr bool kEight = W::kEight, kE4m3 = kStore == KvStore::kE4m3;
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_scan[kWdWarps];
-    __shared__ long long s_start;    // first tile of the unit the range begins in
-    __shared__ int s_b, s_r, s_last;
-
-    grid_dependency_wait();
-    allow_dependent_launch();
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint64_t s_full[kWdWarps][kStages];
+    __shared__ long long s_scan[kWdWarps], s_x[2 * kWdWarps], s_u0[2 * kWdWarps];
+    __shared__ int s_live[kWdWarps], s_b[2 * kWdWarps], s_r[2 * kWdWarps], s_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int units = p.kv_heads * p.row_tiles;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i)
+            mbar_init(smem_u32(&s_full[warp][i]), 1);
+        fence_mbar_init();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
 
-    // ---- this CTA's range of the tile list -------------------------------
-    // Each thread counts the tiles of a contiguous chunk of the sequences; a
-    // block scan gives the total and the chunk the range begins in.
+    // ---- the list of tiles and this CTA's ranges of it --------------------
+    // Each thread counts the tiles of a contiguous chunk of the sequences.
+    const int units = p.kv_heads * p.row_tiles;
     const int per = (p.num_seqs + kWdThreads - 1) / kWdThreads;
     const int sb0 = min(p.num_seqs, tid * per), sb1 = min(p.num_seqs, sb0 + per);
     long long mine = 0;
+    int live = 0;
     for (int b = sb0; b < sb1; ++b) {
         const int len = p.lens[b];
         if ((len < 0 || len > p.max_len) && blockIdx.x == 0)
@@ -214,343 +251,421 @@ __global__ void __launch_bounds__(kWdThreads, 2) window_decode_kernel(const Wind
         WindowView v{};
         v.set<kTile>(len, p.max_len, p.window, p.sinks);
         mine += (long long)v.tiles * units;
+        live += v.tiles > 0;
     }
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long o = __shfl_up_sync(kFullMask, incl, off);
-        if (lane >= off)
-            incl += o;
+        incl += lane >= off ? o : 0;
     }
+    live = __reduce_add_sync(kFullMask, live);
     if (lane == 31)
-        s_scan[warp] = incl;
+        s_scan[warp] = incl, s_live[warp] = live;
     __syncthreads();
-    long long base = 0, total = 0;
+    long long excl = incl - mine, total = 0, all_units = 0;
 #pragma unroll
     for (int w = 0; w < kWdWarps; ++w) {
-        base += w < warp ? s_scan[w] : 0;
+        excl += w < warp ? s_scan[w] : 0;
         total += s_scan[w];
+        all_units += (long long)s_live[w] * units;
     }
     // empty contexts: their rows of out are zero
     for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
         if (p.lens[b] <= 0)
             for (int e = tid; e < p.heads * D / 8; e += kWdThreads)
                 reinterpret_cast<uint4 *>(p.out)[size_t(b) * p.heads * D / 8 + e] = make_uint4(0, 0, 0, 0);
-    const long long ctas = max(1ll, min((long long)gridDim.x, total / p.min_tiles));
-    if (blockIdx.x >= ctas || total == 0)
+    if (total == 0)
         return;
-    const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
-    const long long excl = base + incl - mine;
-    if (excl <= lo && lo < excl + mine) {
-        long long at = excl;
-        for (int b = sb0; b < sb1; ++b) {
-            WindowView v{};
-            v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
-            const long long n = (long long)v.tiles * units;
-            if (lo < at + n) {
-                s_b = b;
-                s_r = int((lo - at) / v.tiles);
-                s_start = at + (long long)s_r * v.tiles;
-                break;
-            }
-            at += n;
-        }
+    const long long warp_ranges =
+        max(1ll, min((long long)gridDim.x * kWdWarps, total / kWdMinTilesWarp));
+    const bool team = warp_ranges > kWdMaxParts * all_units;
+    const long long ranges =
+        team ? max(1ll, min((long long)gridDim.x, total / kWdMinTilesTeam)) : warp_ranges;
+    if (blockIdx.x >= ranges)
+        return;
+    // cuts: thread 2 w (+ 1) finds the begin (end) of warp w's range, or
+    // thread 0 (1) that of the CTA's; the thread whose chunk holds a cut
+    // looks up its unit
+    const int cuts = team ? 2 : 2 * kWdWarps;
+    auto range_of = [&](int w) { return team ? (long long)blockIdx.x : (long long)w * gridDim.x + blockIdx.x; };
+    if (tid < cuts) {
+        const long long i = min(range_of(tid >> 1) + (tid & 1), ranges);
+        s_x[tid] = i * total / ranges;
+        s_b[tid] = 0, s_r[tid] = 0, s_u0[tid] = 0;
     }
     __syncthreads();
+    for (int j = 0; j < cuts; ++j) {
+        long long x = s_x[j];
+        if (x < excl || x >= excl + mine)
+            continue;
+        long long at = excl;
+        int b = sb0;
+        WindowView v{};
+        for (;; ++b) {
+            v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
+            const long long n = (long long)v.tiles * units;
+            if (x < at + n)
+                break;
+            at += n;
+        }
+        int r = int((x - at) / v.tiles);
+        long long u0 = at + (long long)r * v.tiles;
+        const long long before = x - u0, behind = v.tiles - before;
+        if (before <= kWdSnap && before <= behind) {
+            x = u0;
+        } else if (behind <= kWdSnap) {
+            x = u0 = u0 + v.tiles;
+            if (++r == units) {
+                r = 0;
+                do {
+                    ++b;
+                    if (b < p.num_seqs)
+                        v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
+                } while (b < p.num_seqs && v.tiles == 0);
+            }
+        } else if (before <= kWdSnap) {
+            x = u0;
+        }
+        s_x[j] = x, s_b[j] = b, s_r[j] = r, s_u0[j] = u0;
+    }
+    __syncthreads();
+    const int cut = team ? 0 : 2 * warp;
+    const long long range = range_of(warp);
+    const long long lo = s_x[cut], hi = s_x[cut + 1];
+    if (range >= ranges || lo >= hi)
+        return;
 
     WindowSegment seg;
-    seg.b = s_b;
-    seg.r = s_r;
+    seg.b = s_b[cut];
+    seg.r = s_r[cut];
+    seg.u0 = s_u0[cut];
     seg.view.set<kTile>(p.lens[seg.b], p.max_len, p.window, p.sinks);
-    seg.begin = int(lo - s_start);
+    seg.begin = int(lo - seg.u0);
     seg.end = int(min((long long)seg.view.tiles, seg.begin + hi - lo));
     seg.left = hi - lo - (seg.end - seg.begin);
 
     // ---- the warp's stream of tiles --------------------------------------
-    const uint32_t sbase = smem_u32(smem);
-    const uint32_t ring = sbase + uint32_t(warp * kStages) * W::kStageBytes;
-    const uint32_t sring = sbase + W::kOffScales + uint32_t(warp * kStages) * W::kScaleBytes;
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages) * W::kStageBytes;
     const uint64_t policy = l2_policy_evict_first();
+    const int step = team ? kWdWarps : 1, sub = team ? warp : 0;
     const int bs = 1 << p.log2_bs;
-    const unsigned char *kbase = static_cast<const unsigned char *>(p.k);
-    const unsigned char *vbase = static_cast<const unsigned char *>(p.v);
+    const int log2_run = min(p.log2_bs, __ffs(kTile) - 1), run = 1 << log2_run;  // rows of one box
+    const int runs = kTile >> log2_run;
 
     WindowSegment is = seg;        // where the next tile to fetch lies
-    int ii = is.begin + warp;
-    bool more = true;
-    int id = -1;                   // lane j: block of the tile's 8-token group j, if it is seen
+    int ii = is.begin + sub;
+    bool more = true, dead = false;
+    int id = -2;                   // lane j: block of the tile's run j; -2: nothing of it is seen
     auto settle = [&]() {          // move to the warp's next tile and look up its blocks
         while (more && ii >= is.end) {
             more = is.next<kTile>(p, units);
-            ii = is.begin + warp;
+            ii = is.begin + sub;
         }
-        id = -2;                   // -2: nothing of the group is seen
-        if (more && lane < kNT) {
-            const int t = is.view.token<kTile>(ii) + 8 * lane;
-            if (t < is.view.L && (t + 7 >= is.view.ws || t < p.sinks))
+        id = -2;
+        if (more && lane < runs) {
+            const int t = is.view.token<kTile>(ii) + (lane << log2_run);
+            if (t < is.view.L && (t + run > is.view.ws || t < p.sinks))
                 id = __ldg(p.tables + size_t(is.b) * p.max_blocks + (t >> p.log2_bs));
         }
     };
+    float2 coming = make_float2(0.0f, 0.0f);  // lane j: scales of run j of the tile fetched last
     auto issue = [&](int stage) {
-        if (more) {
-            const int t0 = is.view.token<kTile>(ii);
-            const int h = is.r / p.row_tiles;
-            const bool ok = unsigned(id) < unsigned(p.num_blocks);
-            if (id != -2 && !ok)
-                atomicOr(p.err, PA_DEVERR_BLOCK_ID);
-            const int in_block = (t0 + 8 * lane) & (bs - 1);
-            const long long off =
-                ok ? ((((long long)id * p.kv_heads + h) << p.log2_bs) + in_block) * W::kRowBytes : -1;
-            const uint32_t dst = ring + uint32_t(stage) * W::kStageBytes;
-            const int chunk = lane % W::kChunks;
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int row = it * W::kRowsPerCopy + lane / W::kChunks;
-                const long long o = __shfl_sync(kFullMask, off, it * W::kGroups / 8);
-                const bool seen = o >= 0 && is.view.sees(t0 + row, p.sinks);
-                const long long from = seen ? o + (row & 7) * W::kRowBytes + chunk * 16 : 0;
-                const uint32_t to = dst + W::at(row, chunk);
-                cp_async16(to, kbase + from, seen ? 16u : 0u, policy);
-                cp_async16(to + 4096u, vbase + from, seen ? 16u : 0u, policy);
+        if (!more || dead)
+            return;
+        const int t = is.view.token<kTile>(ii) + (lane << log2_run);
+        const int h = is.r / p.row_tiles;
+        const bool ok = unsigned(id) < unsigned(p.num_blocks);
+        if (id != -2 && !ok)
+            atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+        const uint32_t bar = smem_u32(&s_full[warp][stage]);
+        const unsigned there = __ballot_sync(kFullMask, ok);
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, uint32_t(__popc(there)) * uint32_t(2 * W::kRowBytes) << log2_run);
+        __syncwarp();
+        if (ok) {
+            const long long row = (((long long)id * p.kv_heads + h) << p.log2_bs) + (t & (bs - 1));
+            const uint32_t dst = ring + uint32_t(stage) * W::kStageBytes +
+                                 (uint32_t(lane) << log2_run) * uint32_t(W::kRowBytes);
+            if constexpr (kEight) {      // 128-byte lines
+                const int y = int(row * W::kRowBytes / 128);
+                tma_load_2d_hint(dst, &tm_k, 0, y, bar, policy);
+                tma_load_2d_hint(dst + 4096u, &tm_v, 0, y, bar, policy);
+            } else {                     // groups of 8 rows
+                tma_load_4d_hint(dst, &tm_k, 0, 0, 0, int(row >> 3), bar, policy);
+                tma_load_4d_hint(dst + 4096u, &tm_v, 0, 0, 0, int(row >> 3), bar, policy);
             }
-            if constexpr (kEight) {
-                if (lane < kNT)
-                    cp_async8(sring + uint32_t(stage) * W::kScaleBytes + uint32_t(lane) * 8u,
-                              p.scales + (ok ? (long long)id * p.scale_heads + h : 0), ok ? 8u : 0u);
-            }
-            ii += kWdWarps;
-            settle();
         }
-        cp_async_commit();
+        if constexpr (kEight)
+            coming = ok ? __ldg(p.scales + (long long)id * p.scale_heads + h) : make_float2(0.0f, 0.0f);
+        ii += step;
+        settle();
     };
     settle();
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        issue(s);
+    issue(0);
 
     int stage = 0;
-    int nseg = 0;
+    uint32_t phase = 0;
     bool have = true;
     while (have) {
-        const int h = seg.r / p.row_tiles, row0 = (seg.r % p.row_tiles) * 16;
-        const int rows = min(16, p.group - row0);
+        const int h = seg.r / p.row_tiles, row0 = (seg.r % p.row_tiles) * (8 * kNq);
+        const int rows = min(8 * kNq, p.group - row0);
         const size_t out_row = size_t(seg.b) * p.heads + size_t(h) * p.group + row0;
-        const bool two = rows > 8;
 
-        // ---- query rows as the A operand ---------------------------------
-        // a[0], a[2]: row g; a[1], a[3]: row g + 8
-        uint32_t qa[D / 16][4];
-        float f0 = p.scale_log2, f1 = p.scale_log2;
-        {
-            const uint32_t *q0 = reinterpret_cast<const uint32_t *>(
-                static_cast<const uint16_t *>(p.q) + (out_row + g) * D);
-            const uint32_t *q1 = q0 + 8 * D / 2;
+        // ---- query heads as the columns (B operand) ----------------------
+        uint32_t qb[kNq][kDt][2];
+        float f[kNq][2];           // what the scores of columns 2c, 2c + 1 are multiplied by
+#pragma unroll
+        for (int nq = 0; nq < kNq; ++nq) {
+            const bool there = 8 * nq + g < rows;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (out_row + 8 * nq + (there ? g : 0)) * D;
             if constexpr (!kEight) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(src) + c;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    qa[k][0] = g < rows ? __ldg(q0 + 8 * k + c) : 0u;
-                    qa[k][1] = g + 8 < rows ? __ldg(q1 + 8 * k + c) : 0u;
-                    qa[k][2] = g < rows ? __ldg(q0 + 8 * k + c + 4) : 0u;
-                    qa[k][3] = g + 8 < rows ? __ldg(q1 + 8 * k + c + 4) : 0u;
+                for (int k = 0; k < kDt; ++k) {
+                    qb[nq][k][0] = there ? __ldg(w + 8 * k) : 0u;
+                    qb[nq][k][1] = there ? __ldg(w + 8 * k + 4) : 0u;
                 }
+                f[nq][0] = f[nq][1] = p.scale_log2;
             } else {
-                // dims [c D/4, (c + 1) D/4) of a row, 4 per step of the product,
-                // in the order in which the codes are read
-                auto load = [&](const uint32_t *src, bool there, int half, float &f) {
-                    float x[D / 4];
-                    float m = 0.0f;
+                // 16 dims from each 16-byte chunk of codes that the lane reads
+                float x[D / 4];
+                float m = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < D / 8; ++e) {
-                        const uint32_t w = there ? __ldg(src + c * (D / 8) + e) : 0u;
-                        const float2 y = p.bf16 ? Half16<true>::unpack(w) : Half16<false>::unpack(w);
-                        x[2 * e] = y.x;
-                        x[2 * e + 1] = y.y;
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(
+                                                src + (c + 4 * (i >> 1)) * 16 + 8 * (i & 1)))
+                                          : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = p.bf16 ? Half16<true>::unpack(w[e]) : Half16<false>::unpack(w[e]);
+                        x[8 * i + 2 * e] = y.x;
+                        x[8 * i + 2 * e + 1] = y.y;
                         m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
                     }
-                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 1));
-                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 2));
-                    // power of two that brings the largest component to [2^14, 2^15)
-                    const int e2 = m > 0.0f ? min(max(141 - int(__float_as_uint(m) >> 23), -100), 100) : 0;
-                    const float up = __uint_as_float(uint32_t(127 + e2) << 23);
-                    f = p.scale_log2 * __uint_as_float(uint32_t(127 - e2) << 23);
+                }
+                m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 2));
+                // power of two that brings the largest component to [2^14, 2^15)
+                const int e2 = m > 0.0f ? min(max(141 - int(__float_as_uint(m) >> 23), -100), 100) : 0;
+                const float up = __uint_as_float(uint32_t(127 + e2) << 23);
+                const float down = p.scale_log2 * __uint_as_float(uint32_t(127 - e2) << 23);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        qa[k][half] = Half16<false>::pack(x[4 * k] * up, x[4 * k + 1] * up);
-                        qa[k][half + 2] = Half16<false>::pack(x[4 * k + 2] * up, x[4 * k + 3] * up);
-                    }
-                };
-                load(q0, g < rows, 0, f0);
-                load(q1, g + 8 < rows, 1, f1);
+                for (int k = 0; k < kDt; ++k) {
+                    qb[nq][k][0] = Half16<false>::pack(x[4 * k] * up, x[4 * k + 1] * up);
+                    qb[nq][k][1] = Half16<false>::pack(x[4 * k + 2] * up, x[4 * k + 3] * up);
+                }
+                f[nq][0] = __shfl_sync(kFullMask, down, 8 * c);
+                f[nq][1] = __shfl_sync(kFullMask, down, 8 * c + 4);
             }
         }
 
-        float o[D / 8][4];
+        // o[.][dt]: dims of 16-row dt, rows g (x, y) and g + 8 (z, w), columns
+        // 2c (x, z) and 2c + 1 (y, w); m and l of the same columns
+        float o[kNq][kDt][4], m[kNq][2], l[kNq][2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int nq = 0; nq < kNq; ++nq) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[i][e] = 0.0f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-        float sv_ref = 0.0f, sv_inv = 0.0f;
-
-        for (int i = seg.begin + warp; i < seg.end; i += kWdWarps) {
-            cp_async_wait<kStages - 2>();
-            __syncwarp();
-            const uint32_t kt = ring + uint32_t(stage) * W::kStageBytes, vt = kt + 4096u;
-            const uint32_t sc = sring + uint32_t(stage) * W::kScaleBytes;
-            issue(stage == 0 ? kStages - 1 : stage - 1);
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-
-            // ---- scores -----------------------------------------------------
-            float s[kNT][4];
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
+            for (int i = 0; i < kDt; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[j][e] = 0.0f;
-                if constexpr (!kEight) {
+                    o[nq][i][e] = 0.0f;
+            m[nq][0] = m[nq][1] = -INFINITY;
+            l[nq][0] = l[nq][1] = 0.0f;
+        }
+        float sv_ref = 0.0f, sv_inv = 0.0f;
+
+        for (int i = seg.begin + sub; i < seg.end; i += step) {
+            const float2 sc = coming;
+            issue(stage ^ 1);
+            if (!dead && !mbar_wait_bounded(smem_u32(&s_full[warp][stage]), phase)) {
+                atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                dead = true;
+            }
+            dead = __any_sync(kFullMask, dead);
+            const uint32_t kt = ring + uint32_t(stage) * W::kStageBytes, vt = kt + 4096u;
+            const int t0 = seg.view.token<kTile>(i);
+            const bool edge = t0 + kTile > seg.view.L || (t0 < seg.view.ws && t0 + kTile > p.sinks);
+            if (edge) {            // hidden rows of V must not reach the product
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t b[4];
-                        ldmatrix_x4(kt + W::at(8 * j + (lane & 7), 4 * k + (lane >> 3)), b);
-                        mma16816<W::kBf16>(s[j], qa[2 * k], b[0], b[1]);
-                        mma16816<W::kBf16>(s[j], qa[2 * k + 1], b[2], b[3]);
+                for (int e = 0; e < 8; ++e) {
+                    constexpr int kChunks = W::kRowBytes / 16;
+                    const int row = (e * 32 + lane) / kChunks, chunk = (e * 32 + lane) % kChunks;
+                    if (!seg.view.sees(t0 + row, p.sinks))
+                        sts128_zero(vt + W::at(row, chunk));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+
+            // ---- scores: tokens x query heads -----------------------------
+            float s[kMt][kNq][4];
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt) {
+#pragma unroll
+                for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[mt][nq][e] = 0.0f;
+                if constexpr (!kEight) {
+                    const uint32_t base = kt + W::at(16 * mt + (lane & 15), lane >> 4);
+#pragma unroll
+                    for (int k = 0; k < kDt; ++k) {
+                        uint32_t a[4];
+                        ldmatrix_x4((base ^ uint32_t((k & 3) * 32)) + uint32_t(k >> 2) * 1024u, a);
+#pragma unroll
+                        for (int nq = 0; nq < kNq; ++nq)
+                            mma16816<W::kBf16>(s[mt][nq], a, qb[nq][k][0], qb[nq][k][1]);
                     }
                 } else {
+                    uint32_t w[2][kDt];
 #pragma unroll
-                    for (int k = 0; k < D / 64; ++k) {
-                        const uint4 w = lds128(kt + W::at(8 * j + g, c * (D / 64) + k));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                    for (int high = 0; high < 2; ++high)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t b0, b1;
-                            widen4<kE4m3>(ww[e], b0, b1);
-                            mma16816<false>(s[j], qa[4 * k + e], b0, b1);
+                        for (int k = 0; k < D / 64; ++k) {
+                            const uint4 v = lds128(kt + W::at(16 * mt + W::token_of(g, high), c + 4 * k));
+                            w[high][4 * k] = v.x, w[high][4 * k + 1] = v.y;
+                            w[high][4 * k + 2] = v.z, w[high][4 * k + 3] = v.w;
                         }
+#pragma unroll
+                    for (int k = 0; k < kDt; ++k) {
+                        uint32_t a[4];
+                        widen4<kE4m3>(w[0][k], a[0], a[2]);
+                        widen4<kE4m3>(w[1][k], a[1], a[3]);
+#pragma unroll
+                        for (int nq = 0; nq < kNq; ++nq)
+                            mma16816<false>(s[mt][nq], a, qb[nq][k][0], qb[nq][k][1]);
                     }
                 }
             }
-            float ratio[kNT];      // s_v of each 8-token group over the running reference
+            float ratio[kMt][2];   // s_v of rows g, g + 8 over the running reference
             if constexpr (kEight) {
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < kNT; ++j) {
-                    const uint2 w = lds64(sc + uint32_t(j) * 8u);
-                    const float sk = __uint_as_float(w.x);
-                    ratio[j] = __uint_as_float(w.y);
-                    top = fmaxf(top, ratio[j]);
-                    s[j][0] *= f0 * sk;
-                    s[j][1] *= f0 * sk;
-                    s[j][2] *= f1 * sk;
-                    s[j][3] *= f1 * sk;
-                }
-                top = pow2_at_least(top);
+                const float top = pow2_at_least(
+                    __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(fmaxf(sc.y, 0.0f)))));
                 if (top > sv_ref) {
                     const float down = sv_ref / top;
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
+                    for (int nq = 0; nq < kNq; ++nq)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[n][e] *= down;
+                        for (int n = 0; n < kDt; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[nq][n][e] *= down;
                     sv_ref = top;
                     sv_inv = 1.0f / top;
                 }
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
-                    ratio[j] *= sv_inv;
-            } else {
+                for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
+                    for (int high = 0; high < 2; ++high) {
+                        const int from = (16 * mt + W::token_of(g, high)) >> log2_run;
+                        const float sk = __shfl_sync(kFullMask, sc.x, from);
+                        ratio[mt][high] = __shfl_sync(kFullMask, sc.y, from) * sv_inv;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[j][e] *= f0;
-            }
-            const int t0 = seg.view.token<kTile>(i);
-            if (t0 + kTile > seg.view.L || (t0 < seg.view.ws && t0 + kTile > p.sinks)) {
-#pragma unroll
-                for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (!seg.view.sees(t0 + 8 * j + 2 * c + e, p.sinks)) {
-                            s[j][e] = -INFINITY;
-                            s[j][e + 2] = -INFINITY;
+                        for (int nq = 0; nq < kNq; ++nq) {
+                            s[mt][nq][2 * high] *= f[nq][0] * sk;
+                            s[mt][nq][2 * high + 1] *= f[nq][1] * sk;
                         }
-            }
-
-            // ---- running maximum ------------------------------------------
-            float n0 = m0, n1 = m1;
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-                n0 = fmaxf(n0, fmaxf(s[j][0], s[j][1]));
-                n1 = fmaxf(n1, fmaxf(s[j][2], s[j][3]));
-            }
-            n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, 1));
-            n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, 2));
-            if (two) {
-                n1 = fmaxf(n1, __shfl_xor_sync(kFullMask, n1, 1));
-                n1 = fmaxf(n1, __shfl_xor_sync(kFullMask, n1, 2));
+                    }
             } else {
-                n1 = 0.0f;
-            }
-            if (__any_sync(kFullMask, n0 > m0 || n1 > m1)) {
-                const float a0 = n0 > m0 ? exp2_sfu(m0 - n0) : 1.0f;
-                const float a1 = n1 > m1 ? exp2_sfu(m1 - n1) : 1.0f;
-                l0 *= a0;
-                l1 *= a1;
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[n][0] *= a0;
-                    o[n][1] *= a0;
-                    o[n][2] *= a1;
-                    o[n][3] *= a1;
-                }
-                m0 = n0;
-                m1 = n1;
+                for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+                    for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[mt][nq][e] *= p.scale_log2;
             }
-            // a row whose scores are all -inf so far keeps weights of zero
-            const float z0 = (m0 == -INFINITY ? 0.0f : m0) - kWdShift;
-            const float z1 = (m1 == -INFINITY ? 0.0f : m1) - kWdShift;
+            if (edge) {
+#pragma unroll
+                for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+                    for (int high = 0; high < 2; ++high)
+                        if (!seg.view.sees(t0 + 16 * mt + W::token_of(g, high), p.sinks))
+#pragma unroll
+                            for (int nq = 0; nq < kNq; ++nq)
+                                s[mt][nq][2 * high] = s[mt][nq][2 * high + 1] = -INFINITY;
+            }
 
-            // ---- weights and the product with V ---------------------------
+            // ---- reference of the softmax ---------------------------------
+            bool grows = false;
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) {
-                uint32_t pa[4];
+            for (int nq = 0; nq < kNq; ++nq)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = 2 * k + e;
-                    float w0 = exp2_sfu(s[j][0] - z0), w1 = exp2_sfu(s[j][1] - z0);
-                    l0 += w0 + w1;
-                    float w2 = 0.0f, w3 = 0.0f;
-                    if (two) {
-                        w2 = exp2_sfu(s[j][2] - z1);
-                        w3 = exp2_sfu(s[j][3] - z1);
-                        l1 += w2 + w3;
-                    }
-                    if constexpr (kEight) {
-                        w0 *= ratio[j];
-                        w1 *= ratio[j];
-                        w2 *= ratio[j];
-                        w3 *= ratio[j];
-                    }
-                    pa[2 * e] = Half16<W::kBf16>::pack(w0, w1);
-                    pa[2 * e + 1] = Half16<W::kBf16>::pack(w2, w3);
-                }
-                if constexpr (!kEight) {
+                    float x = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < D / 16; ++n) {
-                        uint32_t b[4];
-                        ldmatrix_x4_trans(vt + W::at(16 * k + (lane & 15), 2 * n + (lane >> 4)), b);
-                        mma16816<W::kBf16>(o[2 * n], pa, b[0], b[1]);
-                        mma16816<W::kBf16>(o[2 * n + 1], pa, b[2], b[3]);
+                    for (int mt = 0; mt < kMt; ++mt)
+                        x = fmaxf(x, fmaxf(s[mt][nq][e], s[mt][nq][e + 2]));
+                    grows |= x > m[nq][e] + kWdRescale;
+                }
+            if (__any_sync(kFullMask, grows)) {
+#pragma unroll
+                for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = m[nq][e];
+#pragma unroll
+                        for (int mt = 0; mt < kMt; ++mt)
+                            x = fmaxf(x, fmaxf(s[mt][nq][e], s[mt][nq][e + 2]));
+                        x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(kFullMask, x, 16));
+                        const float down = x > m[nq][e] ? exp2_sfu(m[nq][e] - x) : 1.0f;
+                        m[nq][e] = x;
+                        l[nq][e] *= down;
+#pragma unroll
+                        for (int n = 0; n < kDt; ++n) {
+                            o[nq][n][e] *= down;
+                            o[nq][n][e + 2] *= down;
+                        }
+                    }
+            }
+
+            // ---- weights and the product with V: dims x query heads --------
+            // a column whose scores are all -inf so far keeps weights of zero
+            float z[kNq][2];
+#pragma unroll
+            for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    z[nq][e] = (m[nq][e] == -INFINITY ? 0.0f : m[nq][e]) - kWdShift;
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt) {
+                uint32_t pb[kNq][2];
+#pragma unroll
+                for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                    for (int high = 0; high < 2; ++high) {
+                        float w0 = exp2_sfu(s[mt][nq][2 * high] - z[nq][0]);
+                        float w1 = exp2_sfu(s[mt][nq][2 * high + 1] - z[nq][1]);
+                        l[nq][0] += w0;
+                        l[nq][1] += w1;
+                        if constexpr (kEight) {
+                            w0 *= ratio[mt][high];
+                            w1 *= ratio[mt][high];
+                        }
+                        pb[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0, w1));
+                    }
+                if constexpr (!kEight) {
+                    const uint32_t base = vt + W::at(16 * mt + (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
+#pragma unroll
+                    for (int n = 0; n < kDt; ++n) {
+                        uint32_t a[4];
+                        ldmatrix_x4_trans((base ^ uint32_t((n & 3) * 32)) + uint32_t(n >> 2) * 1024u, a);
+#pragma unroll
+                        for (int nq = 0; nq < kNq; ++nq)
+                            mma16816<W::kBf16>(o[nq][n], a, pb[nq][0], pb[nq][1]);
                     }
                 } else {
-                    // codes of dims [g D/8, (g + 1) D/8) of tokens 2c, 2c + 1 and
-                    // 2c + 8, 2c + 9; pairs of tokens are interleaved bytewise
+                    // codes of dims [g D/8, (g + 1) D/8) of the four tokens of
+                    // the lane's columns; pairs of tokens interleaved bytewise
                     constexpr int kWords = D / 32;
                     uint32_t w[4][kWords];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int row = 16 * k + 2 * c + (e & 1) + 8 * (e >> 1);
+                        const int row = 16 * mt + W::token_of(2 * c + (e & 1), e >> 1);
                         if constexpr (D == 128) {
                             const uint4 x = lds128(vt + W::at(row, g));
                             w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
@@ -560,157 +675,199 @@ __global__ void __launch_bounds__(kWdThreads, 2) window_decode_kernel(const Wind
                         }
                     }
 #pragma unroll
-                    for (int n = 0; n < kWords; ++n) {
-                        const uint32_t x0 = __byte_perm(w[0][n], w[1][n], 0x5140);
-                        const uint32_t x1 = __byte_perm(w[0][n], w[1][n], 0x7362);
-                        const uint32_t y0 = __byte_perm(w[2][n], w[3][n], 0x5140);
-                        const uint32_t y1 = __byte_perm(w[2][n], w[3][n], 0x7362);
-                        uint32_t b0[4], b1[4];
-                        widen4<kE4m3>(x0, b0[0], b0[1]);
-                        widen4<kE4m3>(x1, b0[2], b0[3]);
-                        widen4<kE4m3>(y0, b1[0], b1[1]);
-                        widen4<kE4m3>(y1, b1[2], b1[3]);
+                    for (int n = 0; n < kWords; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mma16816<false>(o[4 * n + e], pa, b0[e], b1[e]);
-                    }
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t order = e ? 0x7362 : 0x5140;
+                            uint32_t a[4];
+                            widen4<kE4m3>(__byte_perm(w[0][n], w[1][n], order), a[0], a[1]);
+                            widen4<kE4m3>(__byte_perm(w[2][n], w[3][n], order), a[2], a[3]);
+#pragma unroll
+                            for (int nq = 0; nq < kNq; ++nq)
+                                mma16816<false>(o[nq][2 * n + e], a, pb[nq][0], pb[nq][1]);
+                        }
                 }
             }
             __syncwarp();  // the stage may be filled again
+            stage ^= 1;
+            phase ^= stage == 0 ? 1u : 0u;
         }
 
-        // ---- merge the warps' parts of the unit ---------------------------
-        l0 += __shfl_xor_sync(kFullMask, l0, 1);
-        l0 += __shfl_xor_sync(kFullMask, l0, 2);
-        l1 += __shfl_xor_sync(kFullMask, l1, 1);
-        l1 += __shfl_xor_sync(kFullMask, l1, 2);
-        if constexpr (kEight) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[n][e] *= sv_ref;
-        }
-        float2 *ml = reinterpret_cast<float2 *>(smem + W::kOffMl);
-        float *mo = reinterpret_cast<float *>(smem + W::kOffMerge);
+        // ---- the end of the unit, or of the range's part of it --------------
         const bool whole = seg.begin == 0 && seg.end == seg.view.tiles;
-        const int slot = 2 * blockIdx.x + (nseg == 0 ? 0 : 1);
-        constexpr int kPerRow = D / 8;                 // threads per row, 8 dims each
-        // 8 rows and 64 dims at a time
-        for (int pass = 0; pass < (two ? 2 : 1) * (D / 64); ++pass) {
-            const int half = pass / (D / 64), part = pass % (D / 64);
-            __syncthreads();  // the merge buffer is free
-            if (c == 0)
-                ml[warp * 8 + g] = half ? make_float2(m1, l1) : make_float2(m0, l0);
-            float *row = mo + (warp * 8 + g) * W::kPitch;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                const float a = half ? o[n][2] : o[n][0], b = half ? o[n][3] : o[n][1];
-                if constexpr (kEight) {
-                    if (D == 64 || (c >> 1) == part) {
-                        const int d = (2 * c * (D / 8) + n) & 63;
-                        row[d] = a;
-                        row[d + D / 8] = b;
-                    }
-                } else if (n / 8 == part) {
-                    *reinterpret_cast<float2 *>(row + 8 * (n & 7) + 2 * c) = make_float2(a, b);
-                }
-            }
-            __syncthreads();
-            const int rr = tid / 8, dd = (tid % 8) * 8, d0 = part * 64 + dd;
-            if (rr < 8 && half * 8 + rr < rows) {
-                float M = -INFINITY;
+        for (int nq = 0; nq < kNq; ++nq) {
 #pragma unroll
-                for (int w = 0; w < kWdWarps; ++w)
-                    M = fmaxf(M, ml[w * 8 + rr].x);
-                const float z = M == -INFINITY ? 0.0f : M;
-                float l = 0.0f, acc[8] = {};
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int w = 0; w < kWdWarps; ++w) {
-                    const float2 e = ml[w * 8 + rr];
-                    const float f = exp2_sfu(e.x - z);
-                    l += f * e.y;
-                    const float4 *src = reinterpret_cast<const float4 *>(mo + (w * 8 + rr) * W::kPitch + dd);
-                    const float4 x = src[0], y = src[1];
-                    acc[0] += f * x.x, acc[1] += f * x.y, acc[2] += f * x.z, acc[3] += f * x.w;
-                    acc[4] += f * y.x, acc[5] += f * y.y, acc[6] += f * y.z, acc[7] += f * y.w;
-                }
-                if (whole) {
-                    const float inv = 1.0f / l;
-                    const bool bf = kEight ? p.bf16 != 0 : W::kBf16;
-                    uint32_t v[4];
+                for (int off = 4; off < 32; off <<= 1)
+                    l[nq][e] += __shfl_xor_sync(kFullMask, l[nq][e], off);
+            if constexpr (kEight)
+#pragma unroll
+                for (int n = 0; n < kDt; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[e] = bf ? Half16<true>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv)
-                                  : Half16<false>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                               (out_row + half * 8 + rr) * D + d0) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
+                        o[nq][n][e] *= sv_ref;
+        }
+        // 16 dims of 8 query heads, from fragment to rows of out
+        const bool bf = kEight ? p.bf16 != 0 : W::kBf16;
+        auto store = [&](int nq, int n, const float4 &v) {
+            uint32_t lo2 = bf ? Half16<true>::pack(v.x, v.y) : Half16<false>::pack(v.x, v.y);
+            uint32_t hi2 = bf ? Half16<true>::pack(v.z, v.w) : Half16<false>::pack(v.z, v.w);
+            lo2 = movmatrix_trans(lo2);
+            hi2 = movmatrix_trans(hi2);
+            if (8 * nq + g < rows) {
+                uint16_t *dst = static_cast<uint16_t *>(p.out) + (out_row + 8 * nq + g) * D;
+                if constexpr (!kEight) {
+                    *reinterpret_cast<uint32_t *>(dst + 16 * n + 2 * c) = lo2;
+                    *reinterpret_cast<uint32_t *>(dst + 16 * n + 8 + 2 * c) = hi2;
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(
-                        p.part_o + (size_t(slot) * 16 + half * 8 + rr) * D + d0);
-                    __stcg(dst, make_float4(acc[0], acc[1], acc[2], acc[3]));
-                    __stcg(dst + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
-                    if (d0 == 0)
-                        __stcg(p.part_ml + size_t(slot) * 16 + half * 8 + rr, make_float2(M, l));
+                    *reinterpret_cast<uint32_t *>(dst + (D / 8) * (2 * c) + 2 * n) =
+                        __byte_perm(lo2, hi2, 0x5410);
+                    *reinterpret_cast<uint32_t *>(dst + (D / 8) * (2 * c + 1) + 2 * n) =
+                        __byte_perm(lo2, hi2, 0x7632);
                 }
             }
+        };
+        // parts of the unit: the cuts that stayed inside it, and this one's
+        // place among them.  The first part is its range's last segment, the
+        // others are their ranges' first.
+        long long first = 0;
+        int parts = 1;
+        if (!whole) {
+            first = ((seg.u0 + kWdSnap + 1) * ranges + total - 1) / total - 1;
+            parts = int(((seg.u0 + seg.view.tiles - kWdSnap) * ranges + total - 1) / total - 1 - first) + 1;
+        }
+        auto slot_of = [&](int k) { return size_t(2 * (first + k) + (k == 0 ? 1 : 0)); };
+        const size_t slot = slot_of(int(range - first));
+        auto part_o = [&](size_t sl, int nq, int n) {
+            return p.part_o + ((sl * kNq + nq) * kDt + n) * 32 + lane;
+        };
+        auto part_ml = [&](size_t sl, int nq) { return p.part_ml + (sl * kNq + nq) * 4 + c; };
+
+        if (!team) {
+#pragma unroll
+            for (int nq = 0; nq < kNq; ++nq) {
+                if (whole) {
+                    const float i0 = 1.0f / l[nq][0], i1 = 1.0f / l[nq][1];
+#pragma unroll
+                    for (int n = 0; n < kDt; ++n)
+                        store(nq, n, make_float4(o[nq][n][0] * i0, o[nq][n][1] * i1, o[nq][n][2] * i0,
+                                                 o[nq][n][3] * i1));
+                } else if (8 * nq + 2 * c < rows) {
+#pragma unroll
+                    for (int n = 0; n < kDt; ++n)
+                        __stcg(part_o(slot, nq, n),
+                               make_float4(o[nq][n][0], o[nq][n][1], o[nq][n][2], o[nq][n][3]));
+                    if (g == 0)
+                        __stcg(part_ml(slot, nq), make_float4(m[nq][0], l[nq][0], m[nq][1], l[nq][1]));
+                }
+            }
+        } else {
+            float4 *mo = reinterpret_cast<float4 *>(smem + W::kOffMerge);
+            float2 *ml = reinterpret_cast<float2 *>(smem + W::kOffMl);
+#pragma unroll
+            for (int nq = 0; nq < kNq; ++nq)
+#pragma unroll
+                for (int pass = 0; pass < kDt / 4; ++pass) {
+                    __syncthreads();  // the merge buffer is free
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float(&x)[4] = o[nq][4 * pass + i];
+                        mo[(warp * 4 + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                    if (g == 0) {
+                        ml[warp * 8 + 2 * c] = make_float2(m[nq][0], l[nq][0]);
+                        ml[warp * 8 + 2 * c + 1] = make_float2(m[nq][1], l[nq][1]);
+                    }
+                    __syncthreads();
+                    float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWdWarps; ++w) {
+                        M0 = fmaxf(M0, ml[w * 8 + 2 * c].x);
+                        M1 = fmaxf(M1, ml[w * 8 + 2 * c + 1].x);
+                    }
+                    const float z0 = M0 == -INFINITY ? 0.0f : M0, z1 = M1 == -INFINITY ? 0.0f : M1;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int w = 0; w < kWdWarps; ++w) {
+                        const float2 a = ml[w * 8 + 2 * c], b = ml[w * 8 + 2 * c + 1];
+                        const float f0 = exp2_sfu(a.x - z0), f1 = exp2_sfu(b.x - z1);
+                        const float4 x = mo[(w * 4 + warp) * 32 + lane];
+                        l0 += f0 * a.y, l1 += f1 * b.y;
+                        acc.x += f0 * x.x, acc.y += f1 * x.y, acc.z += f0 * x.z, acc.w += f1 * x.w;
+                    }
+                    const int n = 4 * pass + warp;
+                    if (whole) {
+                        const float i0 = 1.0f / l0, i1 = 1.0f / l1;
+                        store(nq, n, make_float4(acc.x * i0, acc.y * i1, acc.z * i0, acc.w * i1));
+                    } else if (8 * nq + 2 * c < rows) {
+                        __stcg(part_o(slot, nq, n), acc);
+                        if (warp == 0 && pass == 0 && g == 0)
+                            __stcg(part_ml(slot, nq), make_float4(M0, l0, M1, l1));
+                    }
+                }
         }
 
-        // ---- a unit shared with other CTAs --------------------------------
+        // ---- the last of a straddling unit's parts merges them ---------------
         if (!whole) {
-            // tiles [u0, u0 + tiles) of the list belong to CTAs first .. last
-            const long long u0 = hi - seg.left - seg.end;
-            const int first = int(((u0 + 1) * ctas - 1) / total);
-            const int last = int(((u0 + seg.view.tiles) * ctas - 1) / total);
-            const int n = last - first + 1;
+            unsigned *ticket = p.tickets + (size_t(seg.b) * units + seg.r);
+            bool last;
             __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                unsigned *ticket = p.tickets + (size_t(seg.b) * units + seg.r);
-                s_last = atomicInc(ticket, unsigned(n - 1)) == unsigned(n - 1);
+            if (team) {
+                __syncthreads();
+                if (tid == 0)
+                    s_last = atomicInc(ticket, unsigned(parts - 1)) == unsigned(parts - 1);
+                __syncthreads();
+                last = s_last;
+            } else {
+                __syncwarp();
+                last = lane == 0 && atomicInc(ticket, unsigned(parts - 1)) == unsigned(parts - 1);
+                last = __shfl_sync(kFullMask, int(last), 0) != 0;
             }
-            __syncthreads();
-            if (s_last) {
+            if (last) {
                 __threadfence();
-                // the first CTA's part is its last segment, unless its range
-                // begins with the unit; the others' is their first
-                const bool head = (long long)first * total / ctas == u0;
-                for (int item = tid; item < rows * kPerRow; item += kWdThreads) {
-                    const int rr = item / kPerRow, d0 = (item % kPerRow) * 8;
-                    auto part = [&](int k) { return size_t(2 * (first + k) + (k == 0 && !head ? 1 : 0)) * 16 + rr; };
-                    float M = -INFINITY;
-#pragma unroll 4
-                    for (int k = 0; k < n; ++k)
-                        M = fmaxf(M, __ldcg(p.part_ml + part(k)).x);
-                    const float z = M == -INFINITY ? 0.0f : M;
-                    float l = 0.0f, acc[8] = {};
-#pragma unroll 4
-                    for (int k = 0; k < n; ++k) {
-                        const float2 e = __ldcg(p.part_ml + part(k));
-                        const float4 *src = reinterpret_cast<const float4 *>(p.part_o + part(k) * D + d0);
-                        const float4 x = __ldcg(src), y = __ldcg(src + 1);
-                        const float f = exp2_sfu(e.x - z);
-                        l += f * e.y;
-                        acc[0] += f * x.x, acc[1] += f * x.y, acc[2] += f * x.z, acc[3] += f * x.w;
-                        acc[4] += f * y.x, acc[5] += f * y.y, acc[6] += f * y.z, acc[7] += f * y.w;
-                    }
-                    const float inv = 1.0f / l;
-                    const bool bf = kEight ? p.bf16 != 0 : W::kBf16;
-                    uint32_t v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = bf ? Half16<true>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv)
-                                  : Half16<false>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (out_row + rr) * D + d0) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
+                for (int nq = 0; nq < kNq; ++nq) {
+                    const bool there = 8 * nq + 2 * c < rows;
+                    const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+                    float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+#pragma unroll 8
+                    for (int k = 0; k < parts; ++k) {
+                        const float4 e = there ? __ldcg(part_ml(slot_of(k), nq)) : none;
+                        M0 = fmaxf(M0, e.x), M1 = fmaxf(M1, e.z);
+                    }
+                    const float z0 = M0 == -INFINITY ? 0.0f : M0, z1 = M1 == -INFINITY ? 0.0f : M1;
+#pragma unroll
+                    for (int n = 0; n < kDt; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[nq][n][e] = 0.0f;
+                    // a CTA's warps take every fourth 16 dims each
+#pragma unroll 4
+                    for (int k = 0; k < parts; ++k) {
+                        const float4 e = there ? __ldcg(part_ml(slot_of(k), nq)) : none;
+                        const float f0 = exp2_sfu(e.x - z0), f1 = exp2_sfu(e.z - z1);
+                        l0 += f0 * e.y, l1 += f1 * e.w;
+#pragma unroll
+                        for (int n = 0; n < kDt; ++n)
+                            if (there && (!team || (n & 3) == warp)) {
+                                const float4 x = __ldcg(part_o(slot_of(k), nq, n));
+                                o[nq][n][0] += f0 * x.x, o[nq][n][1] += f1 * x.y;
+                                o[nq][n][2] += f0 * x.z, o[nq][n][3] += f1 * x.w;
+                            }
+                    }
+                    const float i0 = 1.0f / l0, i1 = 1.0f / l1;
+#pragma unroll
+                    for (int n = 0; n < kDt; ++n)
+                        if (!team || (n & 3) == warp)
+                            store(nq, n, make_float4(o[nq][n][0] * i0, o[nq][n][1] * i1,
+                                                     o[nq][n][2] * i0, o[nq][n][3] * i1));
                 }
             }
         }
-        ++nseg;
         have = seg.next<kTile>(p, units);
     }
-    cp_async_wait<0>();
 }
 
 } // namespace pa

@@ -25,6 +25,9 @@ STORES = [(F16, None), (BF16, None), (F16, "int8"), (BF16, "e4m3"), (BF16, "int8
     ([513, 40], 128, 1, 128, 128, 300, 130),
     ([3000, 2999], 10, 2, 128, 16, 4000, 0),
     ([77] * 40, 6, 6, 64, 16, 20, 1000),
+    ([100, 7, 333, 64], 12, 2, 64, 8, 150, 9),
+    ([2500, 100] * 30, 24, 12, 128, 32, 1500, 33),
+    ([300] * 9 + [0, 1], 18, 2, 64, 16, 300, 0),
 ])
 def test_against_64_bits(dtype, codes, lens, heads, kvh, d, bs, window, sinks):
     paged = Paged(lens, kvh, d, bs, dtype, seed=len(lens) * 7 + d, codes=codes)

@@ -109,10 +109,11 @@ def attention_bound(ref, mass, q_dtype, weight_dtype, worst_v=0.0, tokens=0):
     under 2^-13 for the unit-variance rows used here (sum |q_d k_d| scale stays
     below 8); an error e of a score changes its weight by e and the total by as
     much, so 2^-12 of the mass, which also covers the 2^-22 of the
-    exponential.  Weights below the 16-bit type's normal range are off by at
-    most 2^-38 of the largest weight each (tokens, times the largest |V|)."""
+    exponential.  Weights are stored 2^7 times the softmax's or more, so those
+    below fp16's normal range are off by half its last step, 2^-25, and so by
+    2^-32 of the largest weight each (tokens, times the largest |V|)."""
     u_w, u_o = half_step(weight_dtype), half_step(q_dtype)
-    inner = (u_w + 2.0 ** -12) * mass + tokens * 2.0 ** -38 * worst_v
+    inner = (u_w + 2.0 ** -12) * mass + tokens * 2.0 ** -32 * worst_v
     tiny = torch.finfo(q_dtype).smallest_normal * half_step(q_dtype)
     return inner + u_o * (ref.abs() + inner) + tiny
 
