@@ -81,9 +81,9 @@ constexpr int kWdMaxCtas = 512;
 constexpr int kWdMaxRanges = kWdMaxCtas * kWdWarps;
 constexpr float kWdShift = 7.0f;     // weights are 2^7 times the softmax's
 constexpr float kWdRescale = 8.0f;   // move the reference only past this growth
-// Least tiles of a range: a part of a unit costs about as much as 2 tiles
-// (its write, the counter, its share of the merge).
-constexpr int kWdMinTilesWarp = 4, kWdMinTilesTeam = 8;
+// Least tiles of a range, unless the units are smaller: a part of a unit costs
+// about as much as 2 tiles (its write, the counter, its share of the merge).
+constexpr int kWdMinTilesWarp = 2, kWdMinTilesTeam = 8;
 constexpr int kWdSnap = 2;           // cuts this close to a unit's end move there
 constexpr int kWdMaxParts = 8;       // parts a unit may have on average with warp ranges
 
@@ -214,6 +214,93 @@ __device__ __forceinline__ float pow2_at_least(float x)
 }
 
 
+// Joins a unit's parts, in order: for each 8 query heads the fragments n0,
+// n0 + kStride, ... (kCount of them).  Lane (g, c) looks up the m and l of
+// columns 2c, 2c + 1 of parts g, g + 8, ... of 32 at a time.
+template <int kCount, int kStride, typename Slot, typename Ml, typename Part, typename Store>
+__device__ __forceinline__ void merge_parts(int parts, Slot slot_of, Ml part_ml,
+                                            Part part_o, Store store, int columns8, int n0, int lane,
+                                            int rows)
+{
+    constexpr int kAhead = kCount >= 8 ? 2 : kCount >= 4 ? 4 : 8;  // parts whose loads are in flight
+    const int g = lane >> 2, c = lane & 3;
+    for (int nq = 0; nq < columns8; ++nq) {
+        const bool there = 8 * nq + 2 * c < rows;
+        const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        float4 acc[kCount];
+#pragma unroll
+        for (int n = 0; n < kCount; ++n)
+            acc[n] = zero;
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            float4 e[4];
+            float x0 = M0, x1 = M1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + 8 * i + g;
+                e[i] = there && k < parts ? __ldcg(part_ml(slot_of(k), nq)) : none;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x0 = fmaxf(x0, e[i].x), x1 = fmaxf(x1, e[i].z);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(kFullMask, x0, off));
+                x1 = fmaxf(x1, __shfl_xor_sync(kFullMask, x1, off));
+            }
+            const float z0 = x0 == -INFINITY ? 0.0f : x0, z1 = x1 == -INFINITY ? 0.0f : x1;
+            const float d0 = exp2_sfu(M0 - z0), d1 = exp2_sfu(M1 - z1);
+            M0 = x0, M1 = x1;
+            l0 *= d0, l1 *= d1;
+#pragma unroll
+            for (int n = 0; n < kCount; ++n)
+                acc[n].x *= d0, acc[n].y *= d1, acc[n].z *= d0, acc[n].w *= d1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[i].x = exp2_sfu(e[i].x - z0), e[i].z = exp2_sfu(e[i].z - z1);
+                l0 += e[i].x * e[i].y, l1 += e[i].z * e[i].w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (k0 + 8 * i >= parts)
+                    break;
+#pragma unroll
+                for (int k = 0; k < 8; k += kAhead) {
+                    float4 x[kAhead][kCount];
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                        for (int n = 0; n < kCount; ++n)
+                            x[j][n] = there && k0 + 8 * i + k + j < parts
+                                          ? __ldcg(part_o(slot_of(k0 + 8 * i + k + j), nq, n0 + kStride * n))
+                                          : zero;
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) {
+                        const float f0 = __shfl_sync(kFullMask, e[i].x, 4 * (k + j) + c);
+                        const float f1 = __shfl_sync(kFullMask, e[i].z, 4 * (k + j) + c);
+#pragma unroll
+                        for (int n = 0; n < kCount; ++n) {
+                            acc[n].x += f0 * x[j][n].x, acc[n].y += f1 * x[j][n].y;
+                            acc[n].z += f0 * x[j][n].z, acc[n].w += f1 * x[j][n].w;
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(kFullMask, l0, off);
+            l1 += __shfl_xor_sync(kFullMask, l1, off);
+        }
+        const float i0 = 1.0f / l0, i1 = 1.0f / l1;
+#pragma unroll
+        for (int n = 0; n < kCount; ++n)
+            store(nq, n0 + kStride * n,
+                  make_float4(acc[n].x * i0, acc[n].y * i1, acc[n].z * i0, acc[n].w * i1));
+    }
+}
+
 template <KvStore kStore, int D, int kNq>
 __global__ void __launch_bounds__(kWdThreads, 3)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -224,8 +311,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     constexpr bool kEight = W::kEight, kE4m3 = kStore == KvStore::kE4m3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_full[kWdWarps][kStages];
-    __shared__ long long s_scan[kWdWarps], s_x[2 * kWdWarps], s_u0[2 * kWdWarps];
-    __shared__ int s_live[kWdWarps], s_b[2 * kWdWarps], s_r[2 * kWdWarps], s_last;
+    __shared__ long long s_scan[kWdWarps], s_excl[kWdThreads];
+    __shared__ int s_live[kWdWarps], s_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -270,52 +357,55 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         total += s_scan[w];
         all_units += (long long)s_live[w] * units;
     }
-    // empty contexts: their rows of out are zero
-    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
-        if (p.lens[b] <= 0)
-            for (int e = tid; e < p.heads * D / 8; e += kWdThreads)
-                reinterpret_cast<uint4 *>(p.out)[size_t(b) * p.heads * D / 8 + e] = make_uint4(0, 0, 0, 0);
+    s_excl[tid] = excl;
+    __syncthreads();
+    if (all_units < (long long)p.num_seqs * units)  // empty contexts: their rows of out are zero
+        for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
+            if (p.lens[b] <= 0)
+                for (int e = tid; e < p.heads * D / 8; e += kWdThreads)
+                    reinterpret_cast<uint4 *>(p.out)[size_t(b) * p.heads * D / 8 + e] =
+                        make_uint4(0, 0, 0, 0);
     if (total == 0)
         return;
     const long long warp_ranges =
-        max(1ll, min((long long)gridDim.x * kWdWarps, total / kWdMinTilesWarp));
+        min((long long)gridDim.x * kWdWarps, max(total / kWdMinTilesWarp, all_units));
     const bool team = warp_ranges > kWdMaxParts * all_units;
     const long long ranges =
         team ? max(1ll, min((long long)gridDim.x, total / kWdMinTilesTeam)) : warp_ranges;
     if (blockIdx.x >= ranges)
         return;
-    // cuts: thread 2 w (+ 1) finds the begin (end) of warp w's range, or
-    // thread 0 (1) that of the CTA's; the thread whose chunk holds a cut
-    // looks up its unit
-    const int cuts = team ? 2 : 2 * kWdWarps;
-    auto range_of = [&](int w) { return team ? (long long)blockIdx.x : (long long)w * gridDim.x + blockIdx.x; };
-    if (tid < cuts) {
-        const long long i = min(range_of(tid >> 1) + (tid & 1), ranges);
-        s_x[tid] = i * total / ranges;
-        s_b[tid] = 0, s_r[tid] = 0, s_u0[tid] = 0;
-    }
-    __syncthreads();
-    for (int j = 0; j < cuts; ++j) {
-        long long x = s_x[j];
-        if (x < excl || x >= excl + mine)
-            continue;
-        long long at = excl;
-        int b = sb0;
+    const long long range = team ? (long long)blockIdx.x : (long long)warp * gridDim.x + blockIdx.x;
+    if (range >= ranges)
+        return;                    // (no barrier follows for the ranges of warps)
+
+    // ---- the range's two cuts: lane 0 its begin, lane 1 its end -------------
+    long long cut_x = (range + (lane & 1)) * total / ranges, cut_u0 = 0;
+    int cut_b = 0, cut_r = 0;
+    if (lane < 2 && cut_x < total) {
+        int at_thread = 0;         // last thread whose chunk begins at or before the cut
+#pragma unroll
+        for (int half = kWdThreads / 2; half >= 1; half >>= 1)
+            if (s_excl[at_thread + half] <= cut_x)
+                at_thread += half;
+        long long at = s_excl[at_thread];
+        int b = min(p.num_seqs, at_thread * per);
         WindowView v{};
         for (;; ++b) {
             v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
             const long long n = (long long)v.tiles * units;
-            if (x < at + n)
+            if (cut_x < at + n)
                 break;
             at += n;
         }
-        int r = int((x - at) / v.tiles);
-        long long u0 = at + (long long)r * v.tiles;
-        const long long before = x - u0, behind = v.tiles - before;
+        // (a sequence has less than 2^31 tiles a unit, and mostly fewer in all)
+        const long long in = cut_x - at;
+        int r = in <= 0x7fffffff ? int(uint32_t(in) / uint32_t(v.tiles)) : int(in / v.tiles);
+        cut_u0 = at + (long long)r * v.tiles;
+        const long long before = cut_x - cut_u0, behind = v.tiles - before;
         if (before <= kWdSnap && before <= behind) {
-            x = u0;
+            cut_x = cut_u0;
         } else if (behind <= kWdSnap) {
-            x = u0 = u0 + v.tiles;
+            cut_x = cut_u0 = cut_u0 + v.tiles;
             if (++r == units) {
                 r = 0;
                 do {
@@ -325,21 +415,18 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                 } while (b < p.num_seqs && v.tiles == 0);
             }
         } else if (before <= kWdSnap) {
-            x = u0;
+            cut_x = cut_u0;
         }
-        s_x[j] = x, s_b[j] = b, s_r[j] = r, s_u0[j] = u0;
+        cut_b = b, cut_r = r;
     }
-    __syncthreads();
-    const int cut = team ? 0 : 2 * warp;
-    const long long range = range_of(warp);
-    const long long lo = s_x[cut], hi = s_x[cut + 1];
-    if (range >= ranges || lo >= hi)
-        return;
+    const long long lo = __shfl_sync(kFullMask, cut_x, 0), hi = __shfl_sync(kFullMask, cut_x, 1);
+    if (lo >= hi)
+        return;                    // (for a CTA's range, all warps)
 
     WindowSegment seg;
-    seg.b = s_b[cut];
-    seg.r = s_r[cut];
-    seg.u0 = s_u0[cut];
+    seg.b = __shfl_sync(kFullMask, cut_b, 0);
+    seg.r = __shfl_sync(kFullMask, cut_r, 0);
+    seg.u0 = __shfl_sync(kFullMask, cut_u0, 0);
     seg.view.set<kTile>(p.lens[seg.b], p.max_len, p.window, p.sinks);
     seg.begin = int(lo - seg.u0);
     seg.end = int(min((long long)seg.view.tiles, seg.begin + hi - lo));
@@ -827,43 +914,12 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             }
             if (last) {
                 __threadfence();
-#pragma unroll
-                for (int nq = 0; nq < kNq; ++nq) {
-                    const bool there = 8 * nq + 2 * c < rows;
-                    const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-                    float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-#pragma unroll 8
-                    for (int k = 0; k < parts; ++k) {
-                        const float4 e = there ? __ldcg(part_ml(slot_of(k), nq)) : none;
-                        M0 = fmaxf(M0, e.x), M1 = fmaxf(M1, e.z);
-                    }
-                    const float z0 = M0 == -INFINITY ? 0.0f : M0, z1 = M1 == -INFINITY ? 0.0f : M1;
-#pragma unroll
-                    for (int n = 0; n < kDt; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[nq][n][e] = 0.0f;
-                    // a CTA's warps take every fourth 16 dims each
-#pragma unroll 4
-                    for (int k = 0; k < parts; ++k) {
-                        const float4 e = there ? __ldcg(part_ml(slot_of(k), nq)) : none;
-                        const float f0 = exp2_sfu(e.x - z0), f1 = exp2_sfu(e.z - z1);
-                        l0 += f0 * e.y, l1 += f1 * e.w;
-#pragma unroll
-                        for (int n = 0; n < kDt; ++n)
-                            if (there && (!team || (n & 3) == warp)) {
-                                const float4 x = __ldcg(part_o(slot_of(k), nq, n));
-                                o[nq][n][0] += f0 * x.x, o[nq][n][1] += f1 * x.y;
-                                o[nq][n][2] += f0 * x.z, o[nq][n][3] += f1 * x.w;
-                            }
-                    }
-                    const float i0 = 1.0f / l0, i1 = 1.0f / l1;
-#pragma unroll
-                    for (int n = 0; n < kDt; ++n)
-                        if (!team || (n & 3) == warp)
-                            store(nq, n, make_float4(o[nq][n][0] * i0, o[nq][n][1] * i1,
-                                                     o[nq][n][2] * i0, o[nq][n][3] * i1));
-                }
+                // a CTA's warps take every fourth 16 dims each
+                if (team)
+                    merge_parts<kDt / 4, 4>(parts, slot_of, part_ml, part_o, store, kNq, warp, lane,
+                                            rows);
+                else
+                    merge_parts<kDt, 1>(parts, slot_of, part_ml, part_o, store, kNq, 0, lane, rows);
             }
         }
         have = seg.next<kTile>(p, units);
