@@ -217,6 +217,12 @@ __device__ __forceinline__ void umma_commit(uint32_t bar)
 
 // ---- TMA tensor loads -------------------------------------------------------
 
+// Hint: fetch a tensor map that is a kernel parameter.
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Box of a 2-D tensor map at (x = inner element, y = row) into shared memory,
 // completing `bar` by the box's bytes.  x * element size must be a multiple
 // of 16 bytes.
@@ -229,7 +235,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// The same with an L2 eviction-priority policy, from 2-D and 4-D maps.
+// tma_load_2d and tma_load_4d with an L2 eviction-priority policy.
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap *map, int x, int y,
                                                  uint32_t bar, uint64_t policy)
 {

@@ -17,9 +17,9 @@
 
 namespace {
 
-// Two partial-result slots per range (its first and its last unit, the only
-// ones that can straddle ranges), then one merge counter per unit.  The slots
-// have room for the most any call needs, so that the counters of calls that
+// Partial results (two per range: its first and its last unit, the only ones
+// that can straddle ranges), then one merge counter per unit.  The slots have
+// room for the most any call needs, so that the counters of calls that
 // share a workspace always lie in the same place.
 struct WindowWorkspace {
     size_t ml_off, ticket_off, total;
@@ -35,7 +35,7 @@ WindowWorkspace window_workspace(int num_seqs, int num_heads, int num_kv_heads)
 {
     WindowWorkspace w{};
     const int group = num_heads / num_kv_heads, per = unit_heads(group);
-    const size_t slots = size_t(pa::kWdMaxRanges) * 2;
+    const size_t slots = size_t(pa::kWdSlots);
     const size_t units = size_t(num_seqs) * num_kv_heads * ((group + per - 1) / per);
     w.ml_off = align256(slots * 16 * 128 * sizeof(float));
     w.ticket_off = w.ml_off + align256(slots * 16 * sizeof(float2));

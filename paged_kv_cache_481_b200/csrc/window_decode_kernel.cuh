@@ -19,14 +19,19 @@
 //
 // Layout of the work: a "unit" is (sequence, K/V head, 8 * kNq query heads);
 // its visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens
-// at D = 128 in 16 bits).  The tiles of all units, unit after unit, are cut
-// into equal contiguous ranges.  A range belongs to a warp, which then needs
-// nobody else until the end of a unit that straddles ranges, or, when there
-// are so few units that each would be cut into more than 8 parts, to the four
-// warps of a CTA, which take its tiles in turn and merge in shared memory.
-// Cuts within 2 tiles of a unit's end move there.  A straddling unit's parts
-// go to the workspace and the last range to arrive merges them in order, so
-// the result does not depend on the order of arrival.
+// at D = 128 in 16 bits).  The kernel's blocks count the tiles and choose, all
+// alike, one of three ways to share them out:
+//   * much work: the tiles of all units, unit after unit, are cut into equal
+//     contiguous ranges, one a warp, which needs nobody else until the end of
+//     a unit that straddles ranges.  Cuts within 2 tiles of a unit's end move
+//     there.
+//   * few units: each unit is cut into even parts of at least 16 tiles, one a
+//     CTA, whose four warps take its tiles in turn and merge in shared memory.
+//   * little work in many units: the same with parts for single warps.
+// (A second segment or a straddling unit costs a warp 4 us or more, as much as
+// 8 tiles; so little work is better uneven than cut.)  A cut unit's parts go
+// to the workspace and the last one to arrive merges them in order, so the
+// result does not depend on the order of arrival.
 //
 // Each warp keeps a ring of kStages tiles full, across units: one lane per
 // block run issues TMA boxes (K and V) that complete an mbarrier, with the
@@ -46,6 +51,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <climits>
 #include <cstdint>
 
 #include "../../include/pa_window.h"
@@ -69,8 +75,8 @@ struct WindowDecodeParams {
     int log2_bs, num_blocks, scale_heads;
     int bf16;                   // type of q and out
     float scale_log2;           // softmax scale * log2(e)
-    float4 *part_o;             // [2 * ranges][kNq][D / 16][32 lanes]
-    float4 *part_ml;            // [2 * ranges][kNq][4] (m, l) of two query heads
+    float4 *part_o;             // [kWdSlots][kNq][D / 16][32 lanes]
+    float4 *part_ml;            // [kWdSlots][kNq][4] (m, l) of two query heads
     unsigned *tickets;          // [units]
     unsigned *err;
 };
@@ -81,11 +87,11 @@ constexpr int kWdMaxCtas = 512;
 constexpr int kWdMaxRanges = kWdMaxCtas * kWdWarps;
 constexpr float kWdShift = 7.0f;     // weights are 2^7 times the softmax's
 constexpr float kWdRescale = 8.0f;   // move the reference only past this growth
-// Least tiles of a range, unless the units are smaller: a part of a unit costs
-// about as much as 2 tiles (its write, the counter, its share of the merge).
-constexpr int kWdMinTilesWarp = 2, kWdMinTilesTeam = 8;
-constexpr int kWdSnap = 2;           // cuts this close to a unit's end move there
-constexpr int kWdMaxParts = 8;       // parts a unit may have on average with warp ranges
+constexpr int kWdSnap = 2;           // cuts of ranges this close to a unit's end move there
+constexpr int kWdMuchWork = 16;      // tiles a warp from which on ranges are used
+// least tiles of a part: one for a CTA (4 a warp), one for a warp
+constexpr int kWdTeamTiles = 16, kWdWarpTiles = 8;
+constexpr int kWdSlots = 2 * kWdMaxRanges;  // partial results: 2 a range, or 1 a part
 
 template <KvStore kStore, int D>
 struct WindowTraits {
@@ -155,22 +161,71 @@ struct WindowView {
     }
 };
 
-// A stretch [begin, end) of one unit's tiles that belongs to this range, and
-// how much of the range is left behind it.
+// How the tiles are shared out (in shared memory, looked at between segments).
+struct WindowPlan {
+    long long items, total;   // parts; tiles
+    long long workers;        // warps (or CTAs)
+    const long long *before;  // tiles (or parts) before each thread's sequences [kWdThreads]
+    bool ranges;              // contiguous ranges, or parts
+    int chunk;                // most tiles of a part
+    int units;                // units of a sequence
+    int per;                  // sequences per thread in `before`
+};
+
+// A stretch [begin, end) of one unit's tiles for one worker.
 struct WindowSegment {
     int b, r;              // sequence, unit within the sequence
     int begin, end;
-    long long u0;          // number of the unit's first tile in the list
-    long long left;
+    long long item;        // ranges: number of the unit's first tile; else of the part
+    long long left;        // ranges: tiles of the range behind this segment
+    int part, parts;       // not ranges: place among the unit's parts
     WindowView view;
 
-    template <int kTile>
-    __device__ __forceinline__ bool next(const WindowDecodeParams &p, int units)
+    // Number of parts of a unit of `tiles` tiles.
+    static __device__ __forceinline__ int cut(int tiles, int chunk)
     {
+        return int((unsigned(tiles) + unsigned(chunk) - 1) / unsigned(chunk));
+    }
+
+    // The part `item` (its number is set); false behind the last one.
+    template <int kTile>
+    __device__ __forceinline__ bool locate(const WindowDecodeParams &p, const WindowPlan &plan)
+    {
+        if (item >= plan.items)
+            return false;
+        int t = 0;         // last thread whose sequences begin at or before the part
+#pragma unroll
+        for (int half = kWdThreads / 2; half >= 1; half >>= 1)
+            if (plan.before[t + half] <= item)
+                t += half;
+        long long at = plan.before[t];
+        for (b = t * plan.per;; ++b) {
+            view.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
+            parts = cut(view.tiles, plan.chunk);
+            const long long n = (long long)parts * plan.units;
+            if (item < at + n)
+                break;
+            at += n;
+        }
+        const unsigned in = unsigned(item - at);  // parts are fewer than the slots
+        r = int(in / unsigned(parts));
+        part = int(in % unsigned(parts));
+        begin = int((long long)part * view.tiles / parts);
+        end = int((long long)(part + 1) * view.tiles / parts);
+        return true;
+    }
+
+    template <int kTile>
+    __device__ __forceinline__ bool next(const WindowDecodeParams &p, const WindowPlan &plan)
+    {
+        if (!plan.ranges) {
+            item += plan.workers;
+            return locate<kTile>(p, plan);
+        }
         if (left <= 0)
             return false;
-        u0 += view.tiles;
-        if (++r == units) {
+        item += view.tiles;
+        if (++r == plan.units) {
             r = 0;
             do {
                 ++b;
@@ -207,6 +262,11 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
+__device__ __forceinline__ long long ceil_div(long long a, long long b)
+{
+    return (a + b - 1) / b;
+}
+
 // Smallest power of two >= x (x >= 0; infinity stays, NaN gives 0).
 __device__ __forceinline__ float pow2_at_least(float x)
 {
@@ -215,40 +275,37 @@ __device__ __forceinline__ float pow2_at_least(float x)
 
 
 // Joins a unit's parts, in order: for each 8 query heads the fragments n0,
-// n0 + kStride, ... (kCount of them).  Lane (g, c) looks up the m and l of
-// columns 2c, 2c + 1 of parts g, g + 8, ... of 32 at a time.
+// n0 + kStride, ... (kCount of them), kAhead parts' loads in flight.
 template <int kCount, int kStride, typename Slot, typename Ml, typename Part, typename Store>
-__device__ __forceinline__ void merge_parts(int parts, Slot slot_of, Ml part_ml,
-                                            Part part_o, Store store, int columns8, int n0, int lane,
-                                            int rows)
+__device__ __forceinline__ void merge_parts(int parts, Slot slot_of, Ml part_ml, Part part_o, Store store,
+                                            int columns8, int n0, int c, int rows)
 {
-    constexpr int kAhead = kCount >= 8 ? 2 : kCount >= 4 ? 4 : 8;  // parts whose loads are in flight
-    const int g = lane >> 2, c = lane & 3;
+    constexpr int kAhead = kCount >= 8 ? 2 : kCount >= 4 ? 4 : 8;
+    const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
     for (int nq = 0; nq < columns8; ++nq) {
-        const bool there = 8 * nq + 2 * c < rows;
-        const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int most = 8 * nq + 2 * c < rows ? parts : 0;
         float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
         float4 acc[kCount];
 #pragma unroll
         for (int n = 0; n < kCount; ++n)
             acc[n] = zero;
-        for (int k0 = 0; k0 < parts; k0 += 32) {
-            float4 e[4];
+#pragma unroll 1
+        for (int k = 0; k < most; k += kAhead) {
+            float4 e[kAhead], x[kAhead][kCount];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const size_t slot = slot_of(k + j);
+                e[j] = k + j < most ? __ldcg(part_ml(slot, nq)) : none;
+#pragma unroll
+                for (int n = 0; n < kCount; ++n)
+                    x[j][n] = k + j < most ? __ldcg(part_o(slot, nq, n0 + kStride * n)) : zero;
+            }
             float x0 = M0, x1 = M1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = k0 + 8 * i + g;
-                e[i] = there && k < parts ? __ldcg(part_ml(slot_of(k), nq)) : none;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x0 = fmaxf(x0, e[i].x), x1 = fmaxf(x1, e[i].z);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(kFullMask, x0, off));
-                x1 = fmaxf(x1, __shfl_xor_sync(kFullMask, x1, off));
-            }
+            for (int j = 0; j < kAhead; ++j)
+                x0 = fmaxf(x0, e[j].x), x1 = fmaxf(x1, e[j].z);
             const float z0 = x0 == -INFINITY ? 0.0f : x0, z1 = x1 == -INFINITY ? 0.0f : x1;
             const float d0 = exp2_sfu(M0 - z0), d1 = exp2_sfu(M1 - z1);
             M0 = x0, M1 = x1;
@@ -257,42 +314,17 @@ __device__ __forceinline__ void merge_parts(int parts, Slot slot_of, Ml part_ml,
             for (int n = 0; n < kCount; ++n)
                 acc[n].x *= d0, acc[n].y *= d1, acc[n].z *= d0, acc[n].w *= d1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e[i].x = exp2_sfu(e[i].x - z0), e[i].z = exp2_sfu(e[i].z - z1);
-                l0 += e[i].x * e[i].y, l1 += e[i].z * e[i].w;
-            }
+            for (int j = 0; j < kAhead; ++j) {
+                const float f0 = exp2_sfu(e[j].x - z0), f1 = exp2_sfu(e[j].z - z1);
+                l0 += f0 * e[j].y, l1 += f1 * e[j].w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (k0 + 8 * i >= parts)
-                    break;
-#pragma unroll
-                for (int k = 0; k < 8; k += kAhead) {
-                    float4 x[kAhead][kCount];
-#pragma unroll
-                    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                        for (int n = 0; n < kCount; ++n)
-                            x[j][n] = there && k0 + 8 * i + k + j < parts
-                                          ? __ldcg(part_o(slot_of(k0 + 8 * i + k + j), nq, n0 + kStride * n))
-                                          : zero;
-#pragma unroll
-                    for (int j = 0; j < kAhead; ++j) {
-                        const float f0 = __shfl_sync(kFullMask, e[i].x, 4 * (k + j) + c);
-                        const float f1 = __shfl_sync(kFullMask, e[i].z, 4 * (k + j) + c);
-#pragma unroll
-                        for (int n = 0; n < kCount; ++n) {
-                            acc[n].x += f0 * x[j][n].x, acc[n].y += f1 * x[j][n].y;
-                            acc[n].z += f0 * x[j][n].z, acc[n].w += f1 * x[j][n].w;
-                        }
-                    }
+                for (int n = 0; n < kCount; ++n) {
+                    acc[n].x += f0 * x[j][n].x, acc[n].y += f1 * x[j][n].y;
+                    acc[n].z += f0 * x[j][n].z, acc[n].w += f1 * x[j][n].w;
                 }
             }
         }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l0 += __shfl_xor_sync(kFullMask, l0, off);
-            l1 += __shfl_xor_sync(kFullMask, l1, off);
-        }
+        __syncwarp();
         const float i0 = 1.0f / l0, i1 = 1.0f / l1;
 #pragma unroll
         for (int n = 0; n < kCount; ++n)
@@ -311,8 +343,12 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     constexpr bool kEight = W::kEight, kE4m3 = kStore == KvStore::kE4m3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_full[kWdWarps][kStages];
-    __shared__ long long s_scan[kWdWarps], s_excl[kWdThreads];
+    __shared__ long long s_scan[kWdWarps], s_parts[kWdWarps], s_before[kWdThreads];
     __shared__ int s_live[kWdWarps], s_last;
+    __shared__ WindowPlan plan;
+    // of each warp, the segment it works on and the one it fetches; what every
+    // tile needs of them is kept in registers
+    __shared__ WindowSegment s_seg[kWdWarps], s_fetch[kWdWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -320,6 +356,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         for (int i = 0; i < kStages; ++i)
             mbar_init(smem_u32(&s_full[warp][i]), 1);
         fence_mbar_init();
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
     }
     grid_dependency_wait();
     allow_dependent_launch();
@@ -357,8 +395,6 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         total += s_scan[w];
         all_units += (long long)s_live[w] * units;
     }
-    s_excl[tid] = excl;
-    __syncthreads();
     if (all_units < (long long)p.num_seqs * units)  // empty contexts: their rows of out are zero
         for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
             if (p.lens[b] <= 0)
@@ -367,70 +403,102 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                         make_uint4(0, 0, 0, 0);
     if (total == 0)
         return;
-    const long long warp_ranges =
-        min((long long)gridDim.x * kWdWarps, max(total / kWdMinTilesWarp, all_units));
-    const bool team = warp_ranges > kWdMaxParts * all_units;
-    const long long ranges =
-        team ? max(1ll, min((long long)gridDim.x, total / kWdMinTilesTeam)) : warp_ranges;
-    if (blockIdx.x >= ranges)
-        return;
-    const long long range = team ? (long long)blockIdx.x : (long long)warp * gridDim.x + blockIdx.x;
-    if (range >= ranges)
-        return;                    // (no barrier follows for the ranges of warps)
-
-    // ---- the range's two cuts: lane 0 its begin, lane 1 its end -------------
-    long long cut_x = (range + (lane & 1)) * total / ranges, cut_u0 = 0;
-    int cut_b = 0, cut_r = 0;
-    if (lane < 2 && cut_x < total) {
-        int at_thread = 0;         // last thread whose chunk begins at or before the cut
-#pragma unroll
-        for (int half = kWdThreads / 2; half >= 1; half >>= 1)
-            if (s_excl[at_thread + half] <= cut_x)
-                at_thread += half;
-        long long at = s_excl[at_thread];
-        int b = min(p.num_seqs, at_thread * per);
-        WindowView v{};
-        for (;; ++b) {
+    const long long ctas = gridDim.x, warps = ctas * kWdWarps;
+    const bool little = total < kWdMuchWork * warps;
+    const bool team = all_units <= ctas / 4 || (little && all_units <= ctas);
+    const bool ranges = !team && !(little && all_units <= warps);
+    long long items = 0;
+    int chunk = 0;
+    if (!ranges) {                 // the same scan for parts, at most 1.5 a worker
+        const long long even = team ? ceil_div(total, max(ctas - all_units, ctas / 2))
+                                    : ceil_div(2 * total, warps);
+        chunk = max(team ? kWdTeamTiles : kWdWarpTiles, int(min(even, (long long)INT_MAX / 2)));
+        mine = 0;
+        for (int b = sb0; b < sb1; ++b) {
+            WindowView v{};
             v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
-            const long long n = (long long)v.tiles * units;
-            if (cut_x < at + n)
-                break;
-            at += n;
+            mine += (long long)WindowSegment::cut(v.tiles, chunk) * units;
         }
-        // (a sequence has less than 2^31 tiles a unit, and mostly fewer in all)
-        const long long in = cut_x - at;
-        int r = in <= 0x7fffffff ? int(uint32_t(in) / uint32_t(v.tiles)) : int(in / v.tiles);
-        cut_u0 = at + (long long)r * v.tiles;
-        const long long before = cut_x - cut_u0, behind = v.tiles - before;
-        if (before <= kWdSnap && before <= behind) {
-            cut_x = cut_u0;
-        } else if (behind <= kWdSnap) {
-            cut_x = cut_u0 = cut_u0 + v.tiles;
-            if (++r == units) {
-                r = 0;
-                do {
-                    ++b;
-                    if (b < p.num_seqs)
-                        v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
-                } while (b < p.num_seqs && v.tiles == 0);
-            }
-        } else if (before <= kWdSnap) {
-            cut_x = cut_u0;
+        incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(kFullMask, incl, off);
+            incl += lane >= off ? o : 0;
         }
-        cut_b = b, cut_r = r;
+        if (lane == 31)
+            s_parts[warp] = incl;
+        __syncthreads();
+        excl = incl - mine;
+#pragma unroll
+        for (int w = 0; w < kWdWarps; ++w) {
+            excl += w < warp ? s_parts[w] : 0;
+            items += s_parts[w];
+        }
     }
-    const long long lo = __shfl_sync(kFullMask, cut_x, 0), hi = __shfl_sync(kFullMask, cut_x, 1);
-    if (lo >= hi)
-        return;                    // (for a CTA's range, all warps)
+    s_before[tid] = excl;
+    if (tid == 0)
+        plan = WindowPlan{items, total, team ? ctas : warps, s_before, ranges, chunk, units, per};
+    __syncthreads();
+    const long long worker = team ? (long long)blockIdx.x : (long long)warp * ctas + blockIdx.x;
 
     WindowSegment seg;
-    seg.b = __shfl_sync(kFullMask, cut_b, 0);
-    seg.r = __shfl_sync(kFullMask, cut_r, 0);
-    seg.u0 = __shfl_sync(kFullMask, cut_u0, 0);
-    seg.view.set<kTile>(p.lens[seg.b], p.max_len, p.window, p.sinks);
-    seg.begin = int(lo - seg.u0);
-    seg.end = int(min((long long)seg.view.tiles, seg.begin + hi - lo));
-    seg.left = hi - lo - (seg.end - seg.begin);
+    if (!ranges) {
+        seg.item = worker;
+        seg.left = 0;
+        if (!seg.locate<kTile>(p, plan))
+            return;                // (for a CTA's part, all warps)
+    } else {
+        // the range's two cuts: lane 0 its begin, lane 1 its end
+        long long cut_x = (worker + (lane & 1)) * total / warps, cut_u0 = 0;
+        int cut_b = 0, cut_r = 0;
+        if (lane < 2 && cut_x < total) {
+            int t = 0;             // last thread whose sequences begin at or before the cut
+#pragma unroll
+            for (int half = kWdThreads / 2; half >= 1; half >>= 1)
+                if (s_before[t + half] <= cut_x)
+                    t += half;
+            long long at = s_before[t];
+            int b = t * per;
+            WindowView v{};
+            for (;; ++b) {
+                v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
+                const long long n = (long long)v.tiles * units;
+                if (cut_x < at + n)
+                    break;
+                at += n;
+            }
+            int r = int((cut_x - at) / v.tiles);
+            cut_u0 = at + (long long)r * v.tiles;
+            const long long before = cut_x - cut_u0, behind = v.tiles - before;
+            if (before <= kWdSnap && before <= behind) {
+                cut_x = cut_u0;
+            } else if (behind <= kWdSnap) {
+                cut_x = cut_u0 = cut_u0 + v.tiles;
+                if (++r == units) {
+                    r = 0;
+                    do {
+                        ++b;
+                        if (b < p.num_seqs)
+                            v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
+                    } while (b < p.num_seqs && v.tiles == 0);
+                }
+            } else if (before <= kWdSnap) {
+                cut_x = cut_u0;
+            }
+            cut_b = b, cut_r = r;
+        }
+        const long long lo = __shfl_sync(kFullMask, cut_x, 0), hi = __shfl_sync(kFullMask, cut_x, 1);
+        if (lo >= hi)
+            return;
+        seg.b = __shfl_sync(kFullMask, cut_b, 0);
+        seg.r = __shfl_sync(kFullMask, cut_r, 0);
+        seg.item = __shfl_sync(kFullMask, cut_u0, 0);
+        seg.view.set<kTile>(p.lens[seg.b], p.max_len, p.window, p.sinks);
+        seg.begin = int(lo - seg.item);
+        seg.end = int(min((long long)seg.view.tiles, seg.begin + hi - lo));
+        seg.left = hi - lo - (seg.end - seg.begin);
+        seg.part = seg.parts = 0;
+    }
 
     // ---- the warp's stream of tiles --------------------------------------
     const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages) * W::kStageBytes;
@@ -440,28 +508,38 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     const int log2_run = min(p.log2_bs, __ffs(kTile) - 1), run = 1 << log2_run;  // rows of one box
     const int runs = kTile >> log2_run;
 
-    WindowSegment is = seg;        // where the next tile to fetch lies
-    int ii = is.begin + sub;
+    int ii = seg.begin + sub;      // the next tile to fetch, of a unit of head fh of sequence fb
+    int f_end = seg.end, fb = seg.b, fh = seg.r / p.row_tiles;
+    WindowView fv = seg.view;
     bool more = true, dead = false;
+    if (lane == 0)
+        s_seg[warp] = s_fetch[warp] = seg;
+    __syncwarp();
     int id = -2;                   // lane j: block of the tile's run j; -2: nothing of it is seen
     auto settle = [&]() {          // move to the warp's next tile and look up its blocks
-        while (more && ii >= is.end) {
-            more = is.next<kTile>(p, units);
-            ii = is.begin + sub;
+        while (more && ii >= f_end) {
+            WindowSegment next = s_fetch[warp];
+            more = next.next<kTile>(p, plan);
+            __syncwarp();
+            if (lane == 0)
+                s_fetch[warp] = next;
+            __syncwarp();
+            ii = next.begin + sub;
+            f_end = next.end, fb = next.b, fh = next.r / p.row_tiles;
+            fv = next.view;
         }
         id = -2;
         if (more && lane < runs) {
-            const int t = is.view.token<kTile>(ii) + (lane << log2_run);
-            if (t < is.view.L && (t + run > is.view.ws || t < p.sinks))
-                id = __ldg(p.tables + size_t(is.b) * p.max_blocks + (t >> p.log2_bs));
+            const int t = fv.token<kTile>(ii) + (lane << log2_run);
+            if (t < fv.L && (t + run > fv.ws || t < p.sinks))
+                id = __ldg(p.tables + size_t(fb) * p.max_blocks + (t >> p.log2_bs));
         }
     };
     float2 coming = make_float2(0.0f, 0.0f);  // lane j: scales of run j of the tile fetched last
     auto issue = [&](int stage) {
         if (!more || dead)
             return;
-        const int t = is.view.token<kTile>(ii) + (lane << log2_run);
-        const int h = is.r / p.row_tiles;
+        const int t = fv.token<kTile>(ii) + (lane << log2_run);
         const bool ok = unsigned(id) < unsigned(p.num_blocks);
         if (id != -2 && !ok)
             atomicOr(p.err, PA_DEVERR_BLOCK_ID);
@@ -471,7 +549,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             mbar_arrive_expect_tx(bar, uint32_t(__popc(there)) * uint32_t(2 * W::kRowBytes) << log2_run);
         __syncwarp();
         if (ok) {
-            const long long row = (((long long)id * p.kv_heads + h) << p.log2_bs) + (t & (bs - 1));
+            const long long row = (((long long)id * p.kv_heads + fh) << p.log2_bs) + (t & (bs - 1));
             const uint32_t dst = ring + uint32_t(stage) * W::kStageBytes +
                                  (uint32_t(lane) << log2_run) * uint32_t(W::kRowBytes);
             if constexpr (kEight) {      // 128-byte lines
@@ -484,7 +562,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             }
         }
         if constexpr (kEight)
-            coming = ok ? __ldg(p.scales + (long long)id * p.scale_heads + h) : make_float2(0.0f, 0.0f);
+            coming = ok ? __ldg(p.scales + (long long)id * p.scale_heads + fh) : make_float2(0.0f, 0.0f);
         ii += step;
         settle();
     };
@@ -495,9 +573,9 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     uint32_t phase = 0;
     bool have = true;
     while (have) {
-        const int h = seg.r / p.row_tiles, row0 = (seg.r % p.row_tiles) * (8 * kNq);
+        const int h = s_seg[warp].r / p.row_tiles, row0 = (s_seg[warp].r % p.row_tiles) * (8 * kNq);
         const int rows = min(8 * kNq, p.group - row0);
-        const size_t out_row = size_t(seg.b) * p.heads + size_t(h) * p.group + row0;
+        const size_t out_row = size_t(s_seg[warp].b) * p.heads + size_t(h) * p.group + row0;
 
         // ---- query heads as the columns (B operand) ----------------------
         uint32_t qb[kNq][kDt][2];
@@ -563,7 +641,9 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         }
         float sv_ref = 0.0f, sv_inv = 0.0f;
 
-        for (int i = seg.begin + sub; i < seg.end; i += step) {
+        const WindowView view = s_seg[warp].view;
+        const int end = s_seg[warp].end;
+        for (int i = s_seg[warp].begin + sub; i < end; i += step) {
             const float2 sc = coming;
             issue(stage ^ 1);
             if (!dead && !mbar_wait_bounded(smem_u32(&s_full[warp][stage]), phase)) {
@@ -572,14 +652,14 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             }
             dead = __any_sync(kFullMask, dead);
             const uint32_t kt = ring + uint32_t(stage) * W::kStageBytes, vt = kt + 4096u;
-            const int t0 = seg.view.token<kTile>(i);
-            const bool edge = t0 + kTile > seg.view.L || (t0 < seg.view.ws && t0 + kTile > p.sinks);
+            const int t0 = view.token<kTile>(i);
+            const bool edge = t0 + kTile > view.L || (t0 < view.ws && t0 + kTile > p.sinks);
             if (edge) {            // hidden rows of V must not reach the product
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     constexpr int kChunks = W::kRowBytes / 16;
                     const int row = (e * 32 + lane) / kChunks, chunk = (e * 32 + lane) % kChunks;
-                    if (!seg.view.sees(t0 + row, p.sinks))
+                    if (!view.sees(t0 + row, p.sinks))
                         sts128_zero(vt + W::at(row, chunk));
                 }
                 fence_proxy_async_smem();
@@ -669,7 +749,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                 for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
                     for (int high = 0; high < 2; ++high)
-                        if (!seg.view.sees(t0 + 16 * mt + W::token_of(g, high), p.sinks))
+                        if (!view.sees(t0 + 16 * mt + W::token_of(g, high), p.sinks))
 #pragma unroll
                             for (int nq = 0; nq < kNq; ++nq)
                                 s[mt][nq][2 * high] = s[mt][nq][2 * high + 1] = -INFINITY;
@@ -781,6 +861,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         }
 
         // ---- the end of the unit, or of the range's part of it --------------
+        WindowSegment seg = s_seg[warp];
         const bool whole = seg.begin == 0 && seg.end == seg.view.tiles;
 #pragma unroll
         for (int nq = 0; nq < kNq; ++nq) {
@@ -816,17 +897,21 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                 }
             }
         };
-        // parts of the unit: the cuts that stayed inside it, and this one's
-        // place among them.  The first part is its range's last segment, the
-        // others are their ranges' first.
-        long long first = 0;
-        int parts = 1;
-        if (!whole) {
-            first = ((seg.u0 + kWdSnap + 1) * ranges + total - 1) / total - 1;
-            parts = int(((seg.u0 + seg.view.tiles - kWdSnap) * ranges + total - 1) / total - 1 - first) + 1;
+        // Parts of the unit, and their slots.  With ranges, the parts lie
+        // between the cuts that stayed inside the unit; the first is its
+        // range's last segment, the others are their ranges' first.
+        long long first = seg.item - seg.part;
+        int parts = seg.parts, part = seg.part;
+        if (ranges && !whole) {
+            first = ceil_div((seg.item + kWdSnap + 1) * plan.workers, plan.total) - 1;
+            parts = int(ceil_div((seg.item + seg.view.tiles - kWdSnap) * plan.workers, plan.total) - 1 -
+                        first) + 1;
+            part = int((long long)warp * gridDim.x + blockIdx.x - first);
         }
-        auto slot_of = [&](int k) { return size_t(2 * (first + k) + (k == 0 ? 1 : 0)); };
-        const size_t slot = slot_of(int(range - first));
+        auto slot_of = [&](int k) {
+            return size_t(ranges ? 2 * (first + k) + (k == 0 ? 1 : 0) : first + k);
+        };
+        const size_t slot = slot_of(part);
         auto part_o = [&](size_t sl, int nq, int n) {
             return p.part_o + ((sl * kNq + nq) * kDt + n) * 32 + lane;
         };
@@ -898,7 +983,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
 
         // ---- the last of a straddling unit's parts merges them ---------------
         if (!whole) {
-            unsigned *ticket = p.tickets + (size_t(seg.b) * units + seg.r);
+            unsigned *ticket = p.tickets + (size_t(seg.b) * plan.units + seg.r);
             bool last;
             __threadfence();
             if (team) {
@@ -916,13 +1001,16 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                 __threadfence();
                 // a CTA's warps take every fourth 16 dims each
                 if (team)
-                    merge_parts<kDt / 4, 4>(parts, slot_of, part_ml, part_o, store, kNq, warp, lane,
-                                            rows);
+                    merge_parts<kDt / 4, 4>(parts, slot_of, part_ml, part_o, store, kNq, warp, c, rows);
                 else
-                    merge_parts<kDt, 1>(parts, slot_of, part_ml, part_o, store, kNq, 0, lane, rows);
+                    merge_parts<kDt, 1>(parts, slot_of, part_ml, part_o, store, kNq, 0, c, rows);
             }
         }
-        have = seg.next<kTile>(p, units);
+        have = seg.next<kTile>(p, plan);
+        __syncwarp();
+        if (lane == 0)
+            s_seg[warp] = seg;
+        __syncwarp();
     }
 }
 
