@@ -3,6 +3,7 @@
 // the kernels of rope_kernel.cuh.  Nothing here allocates device memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/pa_window.h"
@@ -79,18 +80,13 @@ cudaError_t launch_rope(const pa::RopeParams &p, cudaStream_t stream)
 template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 cudaError_t launch_rope_q8(pa::RopeParams p, cudaStream_t stream)
 {
-    // K and V rows of a block are shared by half a CTA each: 4 rows per warp
-    // and sweep at D = 128
-    constexpr int kThreads = 128;
-    p.tokens_per_cta = p.num_tokens <= 512 ? 1 : 16;
-    p.kv_ctas = int64_t((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta) * p.num_kv_heads;
-    const int per_cta = kThreads / (D / 16) * 2;
-    p.q_row_groups = (p.num_heads + per_cta - 1) / per_cta;
-    const int64_t ctas = p.kv_ctas + int64_t(p.num_tokens) * p.q_row_groups;
+    constexpr int kRows = pa::kRopeThreads / (D / 16) * 2, kSpan = 2 * 32 / (D / 16);
+    p.groups = std::max((p.num_heads + kRows - 1) / kRows, (p.num_kv_heads + kSpan - 1) / kSpan);
+    const int64_t ctas = int64_t(p.num_tokens) * p.groups;
     if (ctas > INT32_MAX)
         return cudaErrorInvalidValue;
-    return launch_pdl(pa::rope_and_cache_q8_kernel<D, kBf16, kInterleaved, kE4m3, kThreads>,
-                      dim3(unsigned(ctas)), dim3(kThreads), 0, stream, p);
+    return launch_pdl(pa::rope_and_cache_q8_kernel<D, kBf16, kInterleaved, kE4m3>, dim3(unsigned(ctas)),
+                      dim3(pa::kRopeThreads), 0, stream, p);
 }
 
 } // namespace

@@ -33,9 +33,7 @@ struct RopeParams {
     int rotary, max_position;
     int block_size, num_blocks;
     int scale_heads;                // heads of a block's scale row (kv heads rounded up to even)
-    int tokens_per_cta;             // 8-bit kernel: tokens whose runs one CTA looks after
-    int64_t kv_ctas;                // 8-bit kernel: CTAs of the K/V part (the rest rotate q)
-    int q_row_groups;               // 8-bit kernel: CTAs per token of the q part
+    int groups;                     // 8-bit kernel: CTAs per token
     unsigned int *err;
 };
 
@@ -108,15 +106,13 @@ __device__ __forceinline__ void rotate_pieces(uint4 &v0, uint4 &v1, const UnitAn
                     H::pack(x[14], x[15]));
 }
 
-// A token's slot and position; false (with the reason recorded once) when the
-// token is padding or its indices are outside the pool or the table.
-__device__ __forceinline__ bool token_place(const RopeParams &p, int i, bool report, int64_t &slot,
-                                            int64_t &pos)
+// Whether a token's slot and position are to be worked on; false (with the
+// reason recorded by one thread) when it is padding or they are outside the
+// pool or the table.
+__device__ __forceinline__ bool token_is_live(const RopeParams &p, bool report, int64_t slot, int64_t pos)
 {
-    slot = p.slots[i];
     if (slot < 0)
         return false;
-    pos = p.rotary > 0 ? p.positions[i] : 0;
     unsigned bad = 0;
     if (slot >= int64_t(p.num_blocks) * p.block_size)
         bad |= PA_DEVERR_SLOT;
@@ -130,11 +126,11 @@ __device__ __forceinline__ bool token_place(const RopeParams &p, int i, bool rep
 constexpr int kRopeThreads = 128;
 
 // Rows [row0, row0 + kPasses * rows per pass) of one token: row r < H is
-// query head r, then the K heads, then the V heads.  All loads of a thread's
-// passes are issued before the first result is stored.
+// query head r, then the K heads, then the V heads.  The rows are fetched
+// together with the token's slot and position, so that only the angles wait
+// for another load.
 template <int D, bool kBf16, bool kInterleaved, int kPasses, bool kQueriesOnly, int kThreads>
-__device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0, int64_t slot,
-                                          int64_t pos)
+__device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0)
 {
     constexpr int kUnits = D / 16, kRows = kThreads / kUnits;
     const int u = threadIdx.x % kUnits, r0 = row0 + threadIdx.x / kUnits;
@@ -143,6 +139,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0, 
     const bool turned = u < p.rotary / 16;
     int p0, p1;
     unit_pieces<kInterleaved>(u, p.rotary, p0, p1);
+    const int64_t slot = p.slots[i], pos = p.rotary > 0 ? p.positions[i] : 0;
     uint4 v0[kPasses], v1[kPasses];
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
@@ -159,6 +156,8 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0, 
         v0[k] = *reinterpret_cast<const uint4 *>(src + p0);
         v1[k] = *reinterpret_cast<const uint4 *>(src + p1);
     }
+    if (!token_is_live(p, threadIdx.x == 0 && row0 == 0, slot, pos))
+        return;
     UnitAngles a;
     if (turned)
         load_angles(a, p.cos_sin + pos * p.rotary, p.rotary / 2, u);
@@ -191,67 +190,122 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
     grid_dependency_wait();
     allow_dependent_launch();
     constexpr int kRows = kRopeThreads / (D / 16) * kPasses;
-    int64_t slot, pos;
-    const int i = blockIdx.x;
-    if (!token_place(p, i, threadIdx.x == 0 && blockIdx.y == 0, slot, pos))
-        return;
-    rope_rows<D, kBf16, kInterleaved, kPasses, false, kRopeThreads>(p, i, blockIdx.y * kRows, slot, pos);
+    rope_rows<D, kBf16, kInterleaved, kPasses, false, kRopeThreads>(p, blockIdx.x, blockIdx.y * kRows);
 }
 
 // ------------------------------------------------------- 8-bit block cache
 
-// One run (new tokens i0 .. i0 + n - 1 of one block, consecutive slots from
-// `slot`) and one K/V head: the first half of the CTA's warps does K, the
-// second V.  A first sweep over the rows finds the largest magnitude, a
-// second one writes the codes; the first kKept rows of a thread stay in
-// registers in between, the others are read again (from the caches).
-template <int D, bool kBf16, bool kInterleaved, bool kE4m3, int kThreads>
-__device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n, int64_t slot, int h,
-                                             float (&amax_sm)[2][kThreads / 64])
+// How a row's values become codes: code = round(x a / d).  With a new scale
+// s = m / top that is x top / m, one rounding instead of two (a value exactly
+// between two codes stays there; bf16 rows hold many); else x / s.
+//
+// The quotient is the product with the rounded reciprocal, corrected by its
+// own remainder (Markstein): 4 operations, and correctly rounded as long as
+// nothing underflows, which factors of 2^40 see to.
+struct CodeScale {
+    float a, d, r;
+    float scale;           // what the block's scale becomes
+    bool grown;            // it is not what it was
+
+    __device__ __forceinline__ CodeScale(float m, float old, int first, float top)
+    {
+        scale = __fdiv_rn(m, top);
+        grown = first == 0 || scale > old;
+        scale = grown ? scale : old;
+        d = grown ? m : old;
+        const float by = d > 1e30f ? 0x1p-40f : d < 1e-30f ? 0x1p40f : 1.0f;
+        a = grown ? top * by : by;
+        d *= by;
+        r = d > 0.0f ? __frcp_rn(d) : 0.0f;   // all codes are 0 where the scale is
+    }
+    __device__ __forceinline__ float code(float x) const
+    {
+        const float n = __fmul_rn(x, a), q = __fmul_rn(n, r);
+        return __fmaf_rn(__fmaf_rn(-q, d, n), r, q);
+    }
+    template <bool kE4m3>
+    __device__ __forceinline__ uint2 encode8(const float *x) const
+    {
+        uint2 w;
+        w.x = encode4<kE4m3>(code(x[0]), code(x[1]), code(x[2]), code(x[3]));
+        w.y = encode4<kE4m3>(code(x[4]), code(x[5]), code(x[6]), code(x[7]));
+        return w;
+    }
+};
+
+// Codes of older rows [0, first) of a block whose scale grew, taken to the new
+// scale; this thread's 16 codes of rows r0, r0 + stride, ..., four at a time.
+template <int D, bool kE4m3>
+__device__ __forceinline__ void rescale_rows(uint8_t *codes, int first, float ratio, int r0, int stride,
+                                             int u)
 {
-    constexpr int kUnits = D / 16, kHalf = kThreads / 2, kRows = kHalf / kUnits, kWarps = kHalf / 32;
-    constexpr int kKept = 2;
+#pragma unroll 1
+    for (int r = r0; r < first; r += 4 * stride) {
+        uint4 c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r + j * stride < first)
+                c[j] = *reinterpret_cast<const uint4 *>(codes + (r + j * stride) * D + 16 * u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (r + j * stride >= first)
+                break;
+            const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = decode2<kE4m3>(w[e]), y = decode2<kE4m3>(w[e] >> 16);
+                o[e] = encode4<kE4m3>(__fmul_rn(x.x, ratio), __fmul_rn(x.y, ratio),
+                                      __fmul_rn(y.x, ratio), __fmul_rn(y.y, ratio));
+            }
+            *reinterpret_cast<uint4 *>(codes + (r + j * stride) * D + 16 * u) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// The K or V rows of one run (new tokens i0 .. i0 + n - 1, consecutive slots
+// of one block) of one K/V head, by kLanes lanes (part of a warp, or the two
+// warps that share `both`), D / 16 to a row: a first sweep finds the largest
+// magnitude, a second one writes the codes.  The first kKept rows of a lane
+// stay in registers in between (as they came, rotated twice rather than kept
+// in fp32), the others are read again.
+template <int D, bool kBf16, bool kInterleaved, bool kE4m3, int kLanes, int kKept>
+__device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n, int64_t block, int first,
+                                             int h, bool is_v, int lane, float *both)
+{
+    constexpr int kUnits = D / 16, kRows = kLanes / kUnits;
     constexpr float kTop = code_top<kE4m3>();
-    const int is_v = threadIdx.x / kHalf, ht = threadIdx.x % kHalf;
-    const int u = ht % kUnits, r0 = ht / kUnits;
-    const int KVH = p.num_kv_heads;
+    const int u = lane % kUnits, r0 = lane / kUnits % kRows;
     const bool turned = !is_v && u < p.rotary / 16;
     int p0 = 16 * u, p1 = 16 * u + 8;
     if (!is_v)
         unit_pieces<kInterleaved>(u, p.rotary, p0, p1);
-    const int64_t block = slot / p.block_size;
-    const int first = int(slot % p.block_size);
-    const uint16_t *src = static_cast<const uint16_t *>(is_v ? p.value : p.key) + int64_t(h) * D;
     const int64_t stride = is_v ? p.value_stride : p.key_stride;
+    const uint16_t *src = static_cast<const uint16_t *>(is_v ? p.value : p.key) + i0 * stride + int64_t(h) * D;
     uint8_t *codes = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) +
-                     (block * KVH + h) * p.block_size * D;
-    float2 *scales = p.kv_scales + block * p.scale_heads + h;
-    float *my_scale = reinterpret_cast<float *>(scales) + is_v;
+                     (block * p.num_kv_heads + h) * p.block_size * D;
+    float *my_scale = reinterpret_cast<float *>(p.kv_scales + block * p.scale_heads + h) + is_v;
     const float old = *my_scale;
 
-    auto fetch = [&](int r, float(&x)[16]) {
-        const int64_t i = i0 + r;
-        const uint4 v0 = *reinterpret_cast<const uint4 *>(src + i * stride + p0);
-        const uint4 v1 = *reinterpret_cast<const uint4 *>(src + i * stride + p1);
-        UnitAngles a;
+    auto load = [&](int r, uint4 (&v)[2]) {
+        v[0] = *reinterpret_cast<const uint4 *>(src + r * stride + p0);
+        v[1] = *reinterpret_cast<const uint4 *>(src + r * stride + p1);
+    };
+    auto values = [&](int r, const uint4 (&v)[2], float (&x)[16]) {
         if (turned) {
-            int64_t pos = p.positions[i];
+            int64_t pos = p.positions[i0 + r];
             if (pos < 0 || pos >= p.max_position) {
                 if (u == 0 && h == 0)
                     atomicOr(p.err, PA_DEVERR_POSITION);
                 pos = 0;
             }
+            UnitAngles a;
             load_angles(a, p.cos_sin + pos * p.rotary, p.rotary / 2, u);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                a.c[e] = 1.0f, a.s[e] = 0.0f;
-        }
-        if (turned) {
-            rotate_unit<kBf16, kInterleaved>(v0, v1, a, x);
+            rotate_unit<kBf16, kInterleaved>(v[0], v[1], a, x);
         } else {
             using H = Half16<kBf16>;
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float2 f = H::unpack(w[e]);
@@ -260,139 +314,134 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
             }
         }
     };
-    auto largest = [](const float(&x)[16]) {
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            m = fmaxf(m, fabsf(x[e]));
-        return m;
-    };
 
-    float kept[kKept][16];
-    float m = 0.0f;
+    uint4 kept[kKept][2];
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
-        if (r0 + k * kRows < n) {
-            fetch(r0 + k * kRows, kept[k]);
-            m = fmaxf(m, largest(kept[k]));
+        if (r0 + k * kRows < n)
+            load(r0 + k * kRows, kept[k]);
+    float m = 0.0f;
+    auto largest = [&](int r, const uint4 (&v)[2]) {
+        if (turned) {
+            float x[16];
+            values(r, v, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                m = fmaxf(m, fabsf(x[e]));
+        } else {
+            const float2 x = Half16<kBf16>::unpack(abs_max_pairs<typename Half16<kBf16>::T2>(v[0], v[1]));
+            m = fmaxf(m, fmaxf(x.x, x.y));
         }
-    for (int r = r0 + kKept * kRows; r < n; r += kRows) {
-        float x[16];
-        fetch(r, x);
-        m = fmaxf(m, largest(x));
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
-    __syncthreads();  // the shared maxima of the previous run have been read
-    if ((threadIdx.x & 31) == 0)
-        amax_sm[is_v][ht / 32] = m;
-    __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        m = fmaxf(m, amax_sm[is_v][w]);
-    float scale = __fdiv_rn(m, kTop);
-    if (first > 0)
-        scale = fmaxf(old, scale);
-
-    auto put = [&](int r, const float(&x)[16]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float y[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                y[f] = scale > 0.0f ? __fdiv_rn(x[4 * e + f], scale) : 0.0f;
-            w[e] = encode2<kE4m3>(y[0], y[1]) | (encode2<kE4m3>(y[2], y[3]) << 16);
-        }
-        uint8_t *dst = codes + int64_t(first + r) * D;
-        *reinterpret_cast<uint2 *>(dst + p0) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(dst + p1) = make_uint2(w[2], w[3]);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
         if (r0 + k * kRows < n)
-            put(r0 + k * kRows, kept[k]);
+            largest(r0 + k * kRows, kept[k]);
+#pragma unroll 1
     for (int r = r0 + kKept * kRows; r < n; r += kRows) {
+        uint4 v[2];
+        load(r, v);
+        largest(r, v);
+    }
+    // (within this run's lanes: the lanes of a group agree on their way here)
+    constexpr int kIn = kLanes < 32 ? kLanes : 32;
+    const unsigned group = kIn == 32 ? kFullMask : ((1u << (kIn & 31)) - 1u) << ((lane & 31) / kIn * kIn);
+#pragma unroll
+    for (int off = kIn / 2; off >= 1; off >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(group, m, off));
+    if constexpr (kLanes == 64) {  // (the whole CTA comes here)
+        __syncthreads();           // the last run's maxima have been read
+        if ((lane & 31) == 0)
+            both[lane / 32] = m;
+        __syncthreads();           // also: the old scale has been read
+        m = fmaxf(both[0], both[1]);
+    }
+    const CodeScale scale(m, old, first, kTop);
+
+    auto put = [&](int r, const float (&x)[16]) {
+        uint8_t *dst = codes + (first + r) * D;
+        *reinterpret_cast<uint2 *>(dst + p0) = scale.encode8<kE4m3>(x);
+        *reinterpret_cast<uint2 *>(dst + p1) = scale.encode8<kE4m3>(x + 8);
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (r0 + k * kRows < n) {
+            float x[16];
+            values(r0 + k * kRows, kept[k], x);
+            put(r0 + k * kRows, x);
+        }
+#pragma unroll 1
+    for (int r = r0 + kKept * kRows; r < n; r += kRows) {
+        uint4 v[2];
         float x[16];
-        fetch(r, x);
+        load(r, v);
+        values(r, v, x);
         put(r, x);
     }
-    if (first > 0 && scale > old) {
-        const float ratio = __fdiv_rn(old, scale);
-        for (int r = r0; r < first; r += kRows) {
-            uint4 *row = reinterpret_cast<uint4 *>(codes + int64_t(r) * D + 16 * u);
-            const uint4 c = *row;
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 a = decode2<kE4m3>(w[e]), b = decode2<kE4m3>(w[e] >> 16);
-                o[e] = encode2<kE4m3>(__fmul_rn(a.x, ratio), __fmul_rn(a.y, ratio)) |
-                       (encode2<kE4m3>(__fmul_rn(b.x, ratio), __fmul_rn(b.y, ratio)) << 16);
-            }
-            *row = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-    if (ht == 0 && (first == 0 || scale > old))
-        *my_scale = scale;
+    if (first > 0 && scale.grown)
+        rescale_rows<D, kE4m3>(codes, first, __fdiv_rn(old, scale.scale), r0, kRows, u);
+    if (lane % kLanes == 0 && scale.grown)
+        *my_scale = scale.scale;
 }
 
-// Grid: p.kv_ctas CTAs, each (a stretch of tokens_per_cta tokens, one K/V
-// head) for the runs that begin in the stretch, then num_tokens *
-// q_row_groups CTAs that rotate query rows.
-template <int D, bool kBf16, bool kInterleaved, bool kE4m3, int kThreads>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_q8_kernel(const RopeParams p)
+// Grid: p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
+// query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A token alone in
+// its run (a decode step) has its heads done side by side, D / 16 lanes each
+// for K and for V.  The heads of a longer run are shared out over the CTAs of
+// its first kSpan tokens, a CTA a head (64 threads K, 64 threads V).
+template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(const RopeParams p)
 {
+    __shared__ float both[2][2];
     grid_dependency_wait();
     allow_dependent_launch();
-    __shared__ float amax_sm[2][kThreads / 64];
-    const int64_t cta = blockIdx.x;
-    if (cta >= p.kv_ctas) {
-        constexpr int kPasses = 2, kRows = kThreads / (D / 16) * kPasses;
-        const int64_t k = cta - p.kv_ctas;
-        const int i = int(k / p.q_row_groups), g = int(k % p.q_row_groups);
-        int64_t slot, pos;
-        if (token_place(p, i, threadIdx.x == 0 && g == 0, slot, pos))
-            rope_rows<D, kBf16, kInterleaved, kPasses, true, kThreads>(p, i, g * kRows, slot, pos);
+    constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kSpan = 2 * kHeads;
+    constexpr int kPasses = 2, kRows = kRopeThreads / kUnits * kPasses;
+    const int i = int(blockIdx.x) / p.groups, g = int(blockIdx.x) % p.groups;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    // slots of the kSpan tokens before this one and of those from it on
+    const int j = i - kSpan + lane;
+    const int64_t near = j >= 0 && j < p.num_tokens ? p.slots[j] : -1;
+    if (g * kRows < p.num_heads)
+        rope_rows<D, kBf16, kInterleaved, kPasses, true, kRopeThreads>(p, i, g * kRows);
+    const int h0 = g * kSpan;
+    if (h0 >= p.num_kv_heads)
         return;
-    }
-    const int h = int(cta % p.num_kv_heads);
-    const int t0 = int(cta / p.num_kv_heads) * p.tokens_per_cta;
-    const int t1 = min(p.num_tokens, t0 + p.tokens_per_cta);
-    const int lane = threadIdx.x & 31, bs = p.block_size;
-    const int64_t slots = int64_t(p.num_blocks) * bs;
-    // every warp finds the same runs: token i begins one unless its slot
-    // follows its neighbour's inside the same block
-    for (int base = t0; base < t1; base += 32) {
-        const int mine = base + lane;
-        int64_t s = -1;
-        bool begins = false;
-        if (mine < t1) {
-            s = p.slots[mine];
-            begins = s >= 0 && s < slots &&
-                     (mine == 0 || s % bs == 0 || p.slots[mine - 1] != s - 1);
-        }
-        unsigned heads = __ballot_sync(kFullMask, begins);
-        while (heads) {
-            const int l = __ffs(heads) - 1;
-            heads &= heads - 1;
-            const int i0 = base + l;
-            const int64_t slot = __shfl_sync(kFullMask, s, l);
-            const int most = min(bs - int(slot % bs), p.num_tokens - i0);
-            int n = 0;
-            while (n < most) {  // the run's length, 32 tokens at a time
-                const int j = n + lane;
-                const unsigned same =
-                    __ballot_sync(kFullMask, j < most && p.slots[i0 + j] == slot + j);
-                if (same != kFullMask) {
-                    n += __ffs(~same) - 1;
-                    break;
-                }
-                n += 32;
+    const int64_t slot = __shfl_sync(kFullMask, near, kSpan);
+    const int bs = p.block_size;
+    if (slot < 0 || slot >= int64_t(p.num_blocks) * bs)
+        return;                    // padding, or recorded with the query rows
+    const int64_t block = slot / bs;
+    const int at = int(slot % bs);
+    const unsigned same =
+        __ballot_sync(kFullMask, near == slot + (lane - kSpan) && near >= block * bs && near < (block + 1) * bs);
+    const int before = __clz(~(same << (32 - kSpan)));  // of the tokens before it, those of its run
+    if (before >= kSpan)
+        return;
+    int n = before + __ffs(~(same >> kSpan)) - 1;
+    if (n - before == 32 - kSpan) {  // the run goes on behind the tokens looked at
+        const int most = before + min(bs - at, p.num_tokens - i);
+        while (n < most) {
+            const int k = n + lane;
+            const unsigned more =
+                __ballot_sync(kFullMask, k < most && p.slots[i - before + k] == slot - before + k);
+            if (more != kFullMask) {
+                n += __ffs(~more) - 1;
+                break;
             }
-            quantize_run<D, kBf16, kInterleaved, kE4m3, kThreads>(p, i0, n, slot, h, amax_sm);
+            n += 32;
         }
+    }
+    if (n == 1) {
+        const int h = h0 + warp / 2 * kHeads + lane / kUnits;
+        if (h < p.num_kv_heads)
+            quantize_run<D, kBf16, kInterleaved, kE4m3, kUnits, 1>(p, i, 1, block, at, h, warp & 1, lane,
+                                                                   nullptr);
+    } else {
+        const int end = min(h0 + kSpan, p.num_kv_heads), half = threadIdx.x / 64;
+        for (int h = h0 + before; h < end; h += n)
+            quantize_run<D, kBf16, kInterleaved, kE4m3, 64, 2>(p, i - before, n, block, at - before, h, half,
+                                                               threadIdx.x % 64, both[half]);
     }
 }
 
