@@ -50,7 +50,6 @@
 #include "../../include/pa.h"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
-#include "tile_softmax.cuh"
 
 namespace pa {
 
@@ -113,6 +112,57 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
         }
     }
     return true;
+}
+
+// ---- softmax arithmetic helpers (inline PTX of documented sm_100 forms) ----
+
+__device__ __forceinline__ float max3f(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x on the special-function unit (approximate, subnormal results flushed).
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One S tile row in registers: all 128 scores of this thread's TMEM lane,
+// loaded with one wait.
+struct ScoreRow {
+    uint32_t s[kPN];
+};
+
+__device__ __forceinline__ void load_score_row(uint32_t tS, ScoreRow &r)
+{
+#pragma unroll
+    for (int cc = 0; cc < kPN / 32; ++cc)
+        tmem_load32_into(tS + uint32_t(cc * 32), r.s + cc * 32);
+    tmem_wait_ld();
+}
+
+// Row max of the raw scores; with kMasked only the first `lim` columns count.
+template <bool kMasked>
+__device__ __forceinline__ float score_row_max(const ScoreRow &r, int lim)
+{
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < kPN; i += 8) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float x = __uint_as_float(r.s[i + 2 * a]), y = __uint_as_float(r.s[i + 2 * a + 1]);
+            if (kMasked) {
+                x = i + 2 * a < lim ? x : -INFINITY;
+                y = i + 2 * a + 1 < lim ? y : -INFINITY;
+            }
+            m[a] = max3f(m[a], x, y);
+        }
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // P = 2^(c * s - m) of the row, as fp16 pairs written into TMEM over the

@@ -20,23 +20,27 @@
 // One CTA per SM; a CTA takes its first item from its index and then the
 // items of CTAs that have not started (clusterlaunchcontrol), so the work
 // balances itself without a counter in memory.  An item walks the 128-token
-// context tiles that some row of it sees: the tile in which its first row's
-// window begins, the tiles of the first tokens, the window's others.  The
-// second query tile skips the first one where its window has left it.
+// context tiles that some row of it sees, half a tile (64 tokens) a step: the
+// tile in which its first row's window begins, the tiles of the first tokens,
+// the window's others.  Steps at either end that a query tile does not see
+// are left out for it.
 //
-// Roles in a CTA (10 warps), as pipelines over mbarriers:
+// Roles in a CTA (11 warps), as pipelines over mbarriers:
 //   * warp 8 loads: TMA boxes of Q rows (64 dims x G heads x tq tokens), then
-//     K and V, one box per block run, into a ring of four 128-byte-swizzled
+//     K and V, one box per block run, into a ring of five 128-byte-swizzled
 //     tiles; runs that no row sees are not looked up or read;
-//   * warp 9, one thread: S_t = Q_t K^T into TMEM, O_t += P_t V with P_t read
-//     from TMEM, in the order S_0 PV_0 S_0' PV_1 S_1' so that the matrix unit
-//     works on one tile while the other's softmax runs;
+//   * warps 9 and 10, tile 0 and 1: S_t = Q_t K^T of 64 tokens into one of two
+//     TMEM buffers a query tile, one step ahead, and O_t += P_t V with P_t read
+//     from TMEM, so that the softmax warps do not wait for the matrix unit.
+//     The issue of a product takes about 130 clocks next to busy softmax
+//     warps, twice what the product takes: hence a warp for each tile;
 //   * warps 0-3 / 4-7: softmax of tile 0 / 1, one row per thread (TMEM lane).
-//     Only tiles that cross an edge of the mask pay for it.  Warps without
-//     rows only keep the pipeline's count.
-// TMEM: S0, S1 at columns 0 and 128 (P over S), O0, O1 from column 256.
-// Every wait is bounded; one that runs out records PA_DEVERR_TIMEOUT and ends
-// all roles, after which copies and matrix work in flight are drained.
+//     Only steps that cross an edge of the mask pay for it.  Warps without
+//     rows, and steps a tile does not take part in, only keep the count.
+// TMEM: S_t buffers at columns 128 t and 128 t + 64 (P over S), O_t from
+// column 256.  Every wait is bounded; one that runs out records
+// PA_DEVERR_TIMEOUT and ends all roles, after which copies and matrix work in
+// flight are drained.
 //
 // Choices of fewer bits: P enters the product with V in the cache's 16-bit
 // type, 2^7 times larger than the softmax's weights (below 2^15 with the
@@ -49,9 +53,9 @@
 
 #include "../../include/pa_window.h"
 #include "half_types.cuh"
+#include "mma_sync.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
-#include "tile_softmax.cuh"
 
 namespace pa {
 
@@ -70,16 +74,18 @@ struct WindowPrefillParams {
 namespace wp {
 
 constexpr int kM = 128;               // rows per query tile
-constexpr int kN = 128;               // context tokens per tile
+constexpr int kN = 128;               // context tokens per K / V tile
+constexpr int kHalf = 64;             // context tokens per step
 constexpr int kTiles = 2;             // query tiles per item
-constexpr int kRing = 4;              // K / V tile slots
+constexpr int kRing = 5;              // K / V tile slots
 constexpr int kItemRing = 2;
-constexpr int kItemConsumers = 1 + 8; // the MMA thread and the eight softmax warps
+constexpr int kItemConsumers = 2 + 8; // the matrix warps and the softmax warps
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kThreads = (kMmaWarp + kTiles) * 32;
 constexpr uint32_t kTmemCols = 512, kTmemO = 2 * kN;
 constexpr float kRescaleLog2 = 8.0f;  // move the reference only past this growth
 constexpr float kShift = 7.0f;        // weights are 2^7 times the softmax's
+constexpr int kPolyEvery = 4;         // pairs of weights, of which one is a polynomial
 constexpr float kFloor = -1e30f;      // reference of a row that has seen nothing yet
 
 template <int D>
@@ -99,10 +105,10 @@ struct Item {
     int pos0[kTiles];          // position of the tile's first token
     int lo;                    // first position of the first token's window
     int first, sink_tiles;     // context tile of lo; tiles of first tokens before it
-    int begin[kTiles], end[kTiles];  // steps of the walk that tile t takes part in
-    int steps;                 // 0: no more items
+    int begin[kTiles], end[kTiles];  // steps (half tiles) of the walk that tile t takes part in
+    int tiles;                 // context tiles of the walk; 0: no more items
 
-    // Context tile of step j: the window's first, the first tokens', the rest.
+    // Context tile j of the walk: the window's first, the first tokens', the rest.
     __device__ __forceinline__ int tile(int j) const
     {
         return j == 0 ? first : j <= sink_tiles ? j - 1 : first + j - sink_tiles;
@@ -111,9 +117,11 @@ struct Item {
 
 struct Shared {
     uint64_t item_full[kItemRing], item_empty[kItemRing];
-    uint64_t q_full, q_empty, drain, next_full;
+    uint64_t q_full, q_empty, next_full;
     uint64_t kv_full[kRing], kv_empty[kRing];
-    uint64_t s_full[kTiles], p_full[kTiles], o_full[kTiles], o_empty[kTiles];
+    uint64_t s_full[kTiles][2], p_full[kTiles][2];
+    uint64_t o_mid[kTiles], o_full[kTiles];  // an item's products but the last step's; all of them
+    uint64_t o_empty[kTiles], drain[kTiles];
     alignas(16) uint64_t next[2];  // answer about a CTA that has not started
     Item item[kItemRing];
     uint32_t tmem;
@@ -211,18 +219,23 @@ struct Cursor {
         it.lo = pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
         it.first = it.lo / kN;
         it.sink_tiles = min((min(p.sinks, it.lo) + kN - 1) / kN, it.first);
-        it.steps = 0;
+        it.tiles = 0;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             it.rows[t] = max(0, min(p.tq, n - row0 - t * p.tq));
             it.pos0[t] = pos + t * p.tq;
             const int last = it.pos0[t] + it.rows[t] - 1;
             const int lo_t = max(0, it.pos0[t] - p.window + 1);
-            // the window's first tile is left out where it lies wholly
-            // before the tile's own window and holds no first token
-            it.begin[t] = lo_t >= (it.first + 1) * kN && p.sinks <= it.first * kN ? 1 : 0;
-            it.end[t] = it.rows[t] > 0 ? it.sink_tiles + last / kN + 1 - it.first : 0;
-            it.steps = max(it.steps, it.end[t]);
+            // halves of the window's first tile are left out where they lie
+            // wholly before the tile's own window and hold no first token
+            const int skip = min(lo_t / kHalf - 2 * it.first, 2);
+            it.begin[t] = p.sinks <= it.first * kN ? skip : 0;
+            // (behind the first tokens' tiles the walk goes on with tile first + 1)
+            const int halves = last / kHalf + 1 - 2 * it.first;
+            it.end[t] = it.rows[t] <= 0        ? 0
+                        : it.sink_tiles > 0 ? 2 * it.sink_tiles + max(halves, 2)
+                                            : halves;
+            it.tiles = max(it.tiles, (it.end[t] + 1) / 2);
         }
     }
 };
@@ -274,7 +287,7 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
     bool go = true;
     while (go) {
         Item it;
-        it.steps = 0;
+        it.tiles = 0;
         const bool found = k >= 0 && cursor.find(p, k, lane, it);
         const int slot = items % kItemRing, use = items / kItemRing;
         bool ok = true;
@@ -308,7 +321,7 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
             break;
         ++items;
         const int32_t *trow = p.tables + size_t(it.b) * p.max_blocks;
-        for (int j = 0; go && j < it.steps; ++j) {
+        for (int j = 0; go && j < it.tiles; ++j) {
             // one run of up to a block per lane
             const int tok = it.tile(j) * kN + lane * box;
             const bool seen = lane * box < kN && tok < it.L && (tok + box > it.lo || tok < p.sinks);
@@ -344,7 +357,7 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
                                 kind == 0 ? tm_k : tm_v, 0, 0, 0, y, full);
             }
         }
-        ring += 2 * it.steps;
+        ring += 2 * it.tiles;
         if (!go)
             break;
         if (lane == 0)
@@ -366,115 +379,102 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
 }
 
 // ------------------------------------------------------------ matrix unit
-template <int D, bool kBf16>
+
+// The products of query tile t; the whole warp comes along, one lane issues.
+template <int D, bool kBf16, int t>
 __device__ __forceinline__ void mma_role(const WindowPrefillParams &p, Shared &sh, uint32_t sbase)
 {
     using S = Shape<D>;
-    constexpr uint32_t kIdescS = idesc_16_f32(kM, kN, false, kBf16);
+    constexpr uint32_t kIdescS = idesc_16_f32(kM, kHalf, false, kBf16);
     constexpr uint32_t kIdescO = idesc_16_f32(kM, D, true, kBf16);
     volatile int *abort = &sh.abort;
     const uint32_t tmem = sh.tmem;
-    auto slot_addr = [&](int i) { return sbase + S::kOffRing + uint32_t(i % kRing) * S::kTileBytes; };
-    auto wait_full = [&](int i) {
-        const bool ok = wait_or_abort(smem_u32(&sh.kv_full[i % kRing]), uint32_t(i / kRing) & 1u, abort,
-                                      p.err);
+    const uint32_t leader = elect_one();
+    auto wait = [&](uint64_t &bar, int phase) {
+        const bool ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&bar), uint32_t(phase) & 1u, abort, p.err));
         tc_fence_after_sync();
         return ok;
     };
-    // K: rows of 8-row groups kGroupBytes apart, halves 1 KB apart
-    auto issue_s = [&](int t, uint32_t k_addr) {
-        const uint32_t q_addr = sbase + uint32_t(t) * S::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint32_t hf = uint32_t(k >> 2), kk = uint32_t(k & 3) * 32u;
-            umma_f16(tmem + uint32_t(t) * kN, smem_desc_sw128(q_addr + hf * S::kSub + kk, 16, 1024),
-                     smem_desc_sw128(k_addr + hf * 1024u + kk, 16, S::kGroupBytes), kIdescS, k > 0);
-        }
-        umma_commit(smem_u32(&sh.s_full[t]));
+    auto commit = [&](uint64_t &bar) { umma_commit_if(leader, smem_u32(&bar)); };
+    // half `h` of tile i of the ring
+    auto half_addr = [&](int i, int h) {
+        return sbase + S::kOffRing + uint32_t(i % kRing) * S::kTileBytes + uint32_t(h) * (S::kTileBytes / 2);
     };
-    auto issue_pv = [&](int t, uint32_t v_addr, bool accumulate) {
-        const uint32_t p_tmem = tmem + uint32_t(t) * kN;  // P aliases S
-        const uint32_t o_tmem = tmem + kTmemO + uint32_t(t) * D;
+    const uint64_t q_desc = smem_desc_sw128(sbase + uint32_t(t) * S::kTileBytes, 16, 1024);
+    // K: rows of 8-row groups kGroupBytes apart, 64-dim halves 1 KB apart.
+    // The scores overwrite the weights of the product before the last, which
+    // the matrix unit takes up first: it works in the order of issue.
+    auto issue_s = [&](int buf, uint32_t k_addr) {
+        const uint32_t d = tmem + uint32_t(2 * t + buf) * kHalf;
+        const uint64_t kd = smem_desc_sw128(k_addr, 16, S::kGroupBytes);
 #pragma unroll
-        for (int k = 0; k < kN / 16; ++k)
-            umma_f16_ts(o_tmem, p_tmem + uint32_t(k) * 8u,
-                        smem_desc_sw128(v_addr + uint32_t(k) * 2u * S::kGroupBytes, 1024, S::kGroupBytes),
-                        kIdescO, accumulate || k > 0);
-        umma_commit(smem_u32(&sh.o_full[t]));
+        for (int k = 0; k < D / 16; ++k)
+            umma_f16_if(leader, d, q_desc + ((uint32_t(k >> 2) * S::kSub + uint32_t(k & 3) * 32u) >> 4),
+                        kd + ((uint32_t(k >> 2) * 1024u + uint32_t(k & 3) * 32u) >> 4), kIdescS, k > 0);
+        commit(sh.s_full[t][buf]);
+    };
+    auto issue_pv = [&](int buf, uint32_t v_addr, bool accumulate) {
+        const uint32_t a = tmem + uint32_t(2 * t + buf) * kHalf;  // P aliases S
+        const uint32_t d = tmem + kTmemO + uint32_t(t) * D;
+        const uint64_t vd = smem_desc_sw128(v_addr, 1024, S::kGroupBytes);
+#pragma unroll
+        for (int k = 0; k < kHalf / 16; ++k)
+            umma_f16_ts_if(leader, d, a + uint32_t(k) * 8u, vd + (uint32_t(k) * 2u * S::kGroupBytes >> 4),
+                           kIdescO, accumulate || k > 0);
     };
 
-    int ring = 0;
-    int cnt[kTiles] = {0, 0};       // steps taken per query tile (all items)
-    int t_items[kTiles] = {0, 0};   // items in which query tile t took part
+    int ring = 0, s_cnt = 0, pv_cnt = 0, items = 0;  // (of this tile)
     bool ok = true;
     for (int u = 0; ok; ++u) {
         const int slot = u % kItemRing;
-        if (!wait_or_abort(smem_u32(&sh.item_full[slot]), uint32_t(u / kItemRing) & 1u, abort, p.err))
+        if (!wait(sh.item_full[slot], u / kItemRing))
             break;
-        const int steps = sh.item[slot].steps;
-        const int b0 = sh.item[slot].begin[0], b1 = sh.item[slot].begin[1];
-        const int e0 = sh.item[slot].end[0], e1 = sh.item[slot].end[1];
-        mbar_arrive(smem_u32(&sh.item_empty[slot]));
-        if (steps == 0)
+        const int tiles = sh.item[slot].tiles, begin = sh.item[slot].begin[t], end = sh.item[slot].end[t];
+        __syncwarp();
+        if (leader)
+            mbar_arrive(smem_u32(&sh.item_empty[slot]));
+        if (tiles == 0)
             break;
-        auto in0 = [&](int j) { return j >= b0 && j < e0; };
-        auto in1 = [&](int j) { return j >= b1 && j < e1; };
-        // P V of tile t at step j: the softmax has written P_t, and, at the
-        // tile's first step, the previous item's epilogue has read O_t
-        auto pv = [&](int t, int j, int begin, uint32_t v_addr) {
-            if (j == begin && t_items[t] > 0 &&
-                !wait_or_abort(smem_u32(&sh.o_empty[t]), uint32_t(t_items[t] - 1) & 1u, abort, p.err))
+        // score product of step y, if the tile takes part in it
+        auto scores = [&](int y) {
+            const int i = ring + (y & ~1);
+            if (!(y & 1) && !wait(sh.kv_full[i % kRing], i / kRing))
                 return false;
-            if (!wait_or_abort(smem_u32(&sh.p_full[t]), uint32_t(cnt[t] + j - begin) & 1u, abort, p.err))
-                return false;
-            tc_fence_after_sync();
-            issue_pv(t, v_addr, j > begin);
+            if (y >= begin && y < end)
+                issue_s(s_cnt++ & 1, half_addr(i, y & 1));
+            if (y & 1)
+                commit(sh.kv_empty[i % kRing]);
+            if (y == 2 * tiles - 1)
+                commit(sh.q_empty);
             return true;
         };
-        if (!(ok = wait_or_abort(smem_u32(&sh.q_full), uint32_t(u) & 1u, abort, p.err) &&
-                   wait_full(ring)))
-            break;
-        if (in0(0))
-            issue_s(0, slot_addr(ring));
-        if (in1(0))
-            issue_s(1, slot_addr(ring));
-        umma_commit(smem_u32(&sh.kv_empty[ring % kRing]));
-        if (steps == 1)
-            umma_commit(smem_u32(&sh.q_empty));  // last score product of the item issued
-        for (int j = 0; j < steps; ++j) {
-            const int iv = ring + 2 * j + 1, ik = ring + 2 * j + 2;
-            const bool next = j + 1 < steps;
-            if (!(ok = wait_full(iv)))
-                break;
-            if (in0(j) && !(ok = pv(0, j, b0, slot_addr(iv))))
-                break;
-            if (next) {
-                if (!(ok = wait_full(ik)))
+        ok = wait(sh.q_full, u) && scores(0);
+        for (int y = 0; ok && y < 2 * tiles; ++y) {
+            const int iv = ring + (y & ~1) + 1;
+            ok = (y + 1 >= 2 * tiles || scores(y + 1)) && ((y & 1) || wait(sh.kv_full[iv % kRing], iv / kRing));
+            if (ok && y >= begin && y < end) {
+                // the previous item's epilogue has read O, the softmax has written P
+                const int x = pv_cnt++;
+                ok = (y > begin || items == 0 || wait(sh.o_empty[t], items - 1)) &&
+                     wait(sh.p_full[t][x & 1], x >> 1);
+                if (!ok)
                     break;
-                if (in0(j + 1))
-                    issue_s(0, slot_addr(ik));
+                issue_pv(x & 1, half_addr(iv, y & 1), y > begin);
+                if (y == end - 2)
+                    commit(sh.o_mid[t]);
+                if (y == end - 1)
+                    commit(sh.o_full[t]);
             }
-            if (in1(j) && !(ok = pv(1, j, b1, slot_addr(iv))))
-                break;
-            umma_commit(smem_u32(&sh.kv_empty[iv % kRing]));
-            if (next) {
-                if (in1(j + 1))
-                    issue_s(1, slot_addr(ik));
-                umma_commit(smem_u32(&sh.kv_empty[ik % kRing]));
-                if (j + 2 == steps)
-                    umma_commit(smem_u32(&sh.q_empty));
-            }
+            if (ok && (y & 1))
+                commit(sh.kv_empty[iv % kRing]);
         }
-        if (e0 > 0)
-            cnt[0] += e0 - b0, ++t_items[0];
-        if (e1 > 0)
-            cnt[1] += e1 - b1, ++t_items[1];
-        ring += 2 * steps;
+        items += end > 0;
+        ring += 2 * tiles;
     }
     // every matrix operation issued has finished before TMEM and the shared
     // tiles are released
-    umma_commit(smem_u32(&sh.drain));
-    mbar_wait_bounded(smem_u32(&sh.drain), 0u);
+    commit(sh.drain[t]);
+    mbar_wait_bounded(smem_u32(&sh.drain[t]), 0u);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -488,40 +488,75 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b)
 }
 
 // Columns the row does not see become -inf: it sees [lo, lim) and [0, sinks).
-__device__ __forceinline__ void mask_row(ScoreRow &r, int lo, int lim, int sinks)
+__device__ __forceinline__ void mask_row(uint32_t (&r)[kHalf], int lo, int lim, int sinks)
 {
     const int s = min(sinks, lim);
 #pragma unroll
-    for (int w = 0; w < kN / 32; ++w) {
+    for (int w = 0; w < kHalf / 32; ++w) {
         const uint32_t m = bits_between(lo - 32 * w, lim - 32 * w) | bits_between(0, s - 32 * w);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (!((m >> i) & 1u))
-                r.s[32 * w + i] = 0xff800000u;
+                r[32 * w + i] = 0xff800000u;
     }
 }
 
-// P = 2^(c * s - m) of the row, as 16-bit pairs over the first 64 columns of
-// S; returns the row sum of the unrounded P.
-template <bool kBf16>
-__device__ __forceinline__ float write_weights(uint32_t tS, const ScoreRow &r, float c, float m)
+__device__ __forceinline__ float row_max(const uint32_t (&r)[kHalf])
 {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int cc = 0; cc < kN / 32; ++cc) {
-        uint32_t pk[16];
+    for (int i = 0; i < kHalf; i += 8)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int i = cc * 32 + 2 * e;
-            const float p0 = ex2_approx(fmaf(__uint_as_float(r.s[i]), c, -m));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(r.s[i + 1]), c, -m));
-            sum[(e & 1) * 2] += p0;
-            sum[(e & 1) * 2 + 1] += p1;
-            pk[e] = Half16<kBf16>::pack(p0, p1);
+        for (int a = 0; a < 4; ++a)
+            m[a] = max3f(m[a], __uint_as_float(r[i + 2 * a]), __uint_as_float(r[i + 2 * a + 1]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 2^x of a pair by additions and multiplications: x = n + f with n whole and
+// |f| <= 1/2, a polynomial for 2^f (minimax of the relative error, 2.7e-6) and
+// n added to its exponent.  x below -126 counts as -126.
+__device__ __forceinline__ uint64_t exp2_poly_f32x2(uint64_t x)
+{
+    const float2 v = unpack_f32x2(x);
+    x = pack_f32x2(max_nan(v.x, -126.0f), max_nan(v.y, -126.0f));
+    const uint64_t whole = pack_f32x2(12582912.0f, 12582912.0f);  // 1.5 * 2^23: sums are whole
+    const uint64_t t = add_f32x2(x, whole);
+    const uint64_t f = sub_f32x2(x, sub_f32x2(t, whole));
+    uint64_t y = pack_f32x2(0.009570102207362652f, 0.009570102207362652f);
+    y = fma_f32x2(y, f, pack_f32x2(0.05591786280274391f, 0.05591786280274391f));
+    y = fma_f32x2(y, f, pack_f32x2(0.240247443318367f, 0.240247443318367f));
+    y = fma_f32x2(y, f, pack_f32x2(0.6931217908859253f, 0.6931217908859253f));
+    y = fma_f32x2(y, f, pack_f32x2(0.9999992847442627f, 0.9999992847442627f));
+    const uint32_t lo = uint32_t(y) + (uint32_t(t) << 23), hi = uint32_t(y >> 32) + (uint32_t(t >> 32) << 23);
+    return uint64_t(lo) | uint64_t(hi) << 32;
+}
+
+// P = 2^(c * s - m) of the row, as 16-bit pairs over the first 32 columns of
+// its buffer; returns the row sum of the unrounded P.  One pair in kPolyEvery
+// goes through the polynomial, which takes that share off the special-function
+// unit (4 lanes a clock and quarter of an SM).
+template <bool kBf16>
+__device__ __forceinline__ float write_weights(uint32_t tS, const uint32_t (&r)[kHalf], float c, float m)
+{
+    const uint64_t cc = pack_f32x2(c, c), mm = pack_f32x2(-m, -m);
+    uint64_t sum[2] = {0, 0};
+    uint32_t pk[kHalf / 2];
+#pragma unroll
+    for (int e = 0; e < kHalf / 2; ++e) {
+        uint64_t x = fma_f32x2(uint64_t(r[2 * e]) | uint64_t(r[2 * e + 1]) << 32, cc, mm);
+        if (kPolyEvery > 0 && e % kPolyEvery == kPolyEvery - 1) {
+            x = exp2_poly_f32x2(x);
+        } else {
+            const float2 v = unpack_f32x2(x);
+            x = pack_f32x2(exp2_sfu(v.x), exp2_sfu(v.y));
         }
-        tmem_store16(tS + uint32_t(cc * 16), pk);
+        sum[e & 1] = add_f32x2(sum[e & 1], x);
+        const float2 v = unpack_f32x2(x);
+        pk[e] = Half16<kBf16>::pack(v.x, v.y);
     }
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    tmem_store32(tS, pk);
+    const float2 v = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+    return v.x + v.y;
 }
 
 template <int D, bool kBf16>
@@ -534,10 +569,10 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
     const int r = (warp & 3) * 32 + lane;
     const int r_token = r / p.group, r_head = r % p.group;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = sh.tmem + uint32_t(t) * kN + lane_base;
+    const uint32_t tS = sh.tmem + uint32_t(t) * 2u * kHalf + lane_base;
     const uint32_t tO = sh.tmem + kTmemO + uint32_t(t) * D + lane_base;
     const float c = p.scale_log2;
-    int ring = 0, cnt = 0;
+    int ring = 0, cnt = 0, mid = 0, items = 0;  // steps, items of two steps and more, items (of this tile)
     for (int u = 0;; ++u) {
         const int slot = u % kItemRing;
         if (!__all_sync(kFullMask, wait_or_abort(smem_u32(&sh.item_full[slot]),
@@ -547,10 +582,10 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_u32(&sh.item_empty[slot]));
-        if (it.steps == 0)
+        if (it.tiles == 0)
             break;
         const int item_ring = ring;
-        ring += 2 * it.steps;
+        ring += 2 * it.tiles;
         if (it.rows[t] <= 0)
             continue;
         const bool live = (warp & 3) * 32 < it.rows[t] * p.group;  // the warp holds rows
@@ -559,31 +594,39 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
         const int begin = it.begin[t], end = it.end[t];
         float m_ref = kFloor, l = 0.f;
         bool ok = true;
-        for (int j = begin; j < end; ++j) {
-            ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.s_full[t]),
-                                                     uint32_t(cnt + j - begin) & 1u, abort, p.err));
+        for (int y = begin; y < end; ++y) {
+            const int x = cnt + y - begin, buf = x & 1;
+            ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.s_full[t][buf]), uint32_t(x >> 1) & 1u,
+                                                     abort, p.err));
             if (!ok)
                 break;
             tc_fence_after_sync();
-            const int t0 = it.tile(j) * kN;
+            const int t0 = it.tile(y >> 1) * kN + (y & 1) * kHalf;
             if (live) {
-                ScoreRow row;
-                load_score_row(tS, row);
+                uint32_t row[kHalf];
+                tmem_load32_into(tS + uint32_t(buf) * kHalf, row);
+                tmem_load32_into(tS + uint32_t(buf) * kHalf + 32u, row + 32);
+                tmem_wait_ld();
                 const int lo = my_lo - t0, lim = my_end - t0, sinks = p.sinks - t0;
-                if (__any_sync(kFullMask, lim < kN || (lo > 0 && sinks < kN)))
+                if (__any_sync(kFullMask, lim < kHalf || (lo > 0 && sinks < kHalf)))
                     mask_row(row, lo, lim, sinks);
-                const float m_new = fmaxf(m_ref, score_row_max<false>(row, kN) * c);
-                if (j == begin) {
+                const float m_new = fmaxf(m_ref, row_max(row) * c);
+                if (y == begin) {
                     m_ref = m_new;
                 } else if (__any_sync(kFullMask, m_new > m_ref + kRescaleLog2)) {
-                    // move this warp's reference: rescale O and l
-                    ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.o_full[t]),
-                                                             uint32_t(cnt + j - begin - 1) & 1u, abort,
-                                                             p.err));
+                    // move this warp's reference: rescale O and l,
+                    // once the last step's product is done, which the next
+                    // scores or the end of the item tell
+                    ok = __all_sync(kFullMask,
+                                    y + 1 < end
+                                        ? wait_or_abort(smem_u32(&sh.s_full[t][buf ^ 1]),
+                                                        uint32_t((x + 1) >> 1) & 1u, abort, p.err)
+                                        : wait_or_abort(smem_u32(&sh.o_mid[t]), uint32_t(mid) & 1u, abort,
+                                                        p.err));
                     if (!ok)
                         break;
                     tc_fence_after_sync();
-                    const float alpha = ex2_approx(m_ref - m_new);
+                    const float alpha = exp2_sfu(m_ref - m_new);
 #pragma unroll 1
                     for (int cc = 0; cc < D / 16; ++cc) {  // 16 columns at a time: the score row is live
                         uint32_t o[16];
@@ -597,43 +640,47 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
                     l *= alpha;
                     m_ref = m_new;
                 }
-                l += write_weights<kBf16>(tS, row, c, m_ref - kShift);
+                l += write_weights<kBf16>(tS + uint32_t(buf) * kHalf, row, c, m_ref - kShift);
                 tmem_wait_st();
             }
             // V rows that no row of the item sees (behind the context, before
             // the window, stale ring contents) are zeroed, so that 0 * garbage
-            // cannot reach O.  Done by the first tile that uses the step.
-            if ((t0 + kN > it.L || (t0 < it.lo && t0 + kN > p.sinks)) && t == (j < it.end[0] ? 0 : 1)) {
-                const int iv = item_ring + 2 * j + 1;
+            // cannot reach O: by each tile that takes part in the step, since
+            // either may be first, two threads a row.
+            if (t0 + kHalf > it.L || (t0 < it.lo && t0 + kHalf > p.sinks)) {
+                const int iv = item_ring + (y & ~1) + 1;
                 ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.kv_full[iv % kRing]),
                                                          uint32_t(iv / kRing) & 1u, abort, p.err));
                 if (!ok)
                     break;
-                const int tok = t0 + r;
+                const int vr = r >> 1, tok = t0 + vr;
                 if (!(tok < it.L && (tok >= it.lo || tok < p.sinks))) {
                     unsigned char *at = smem + S::kOffRing + uint32_t(iv % kRing) * S::kTileBytes +
-                                        uint32_t(r >> 3) * S::kGroupBytes + uint32_t(r & 7) * 128u;
+                                        uint32_t(y & 1) * (S::kTileBytes / 2) +
+                                        uint32_t(vr >> 3) * S::kGroupBytes + uint32_t(vr & 7) * 128u;
 #pragma unroll
                     for (int hf = 0; hf < S::kHalves; ++hf)
 #pragma unroll
-                        for (int q16 = 0; q16 < 8; ++q16)
-                            *reinterpret_cast<uint4 *>(at + hf * 1024 + q16 * 16) = make_uint4(0, 0, 0, 0);
+                        for (int q16 = 0; q16 < 4; ++q16)
+                            *reinterpret_cast<uint4 *>(at + hf * 1024 + (r & 1) * 64 + q16 * 16) =
+                                make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(smem_u32(&sh.p_full[t]));
+                mbar_arrive(smem_u32(&sh.p_full[t][buf]));
         }
         if (!ok)
             break;
         // epilogue: out = O / l, then O_t is free for the next item
-        ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.o_full[t]),
-                                                 uint32_t(cnt + end - begin - 1) & 1u, abort, p.err));
+        ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.o_full[t]), uint32_t(items) & 1u, abort, p.err));
         if (!ok)
             break;
         cnt += end - begin;
+        mid += end - begin > 1;
+        ++items;
         if (live) {
             tc_fence_after_sync();
             const float inv = 1.f / l;
@@ -691,18 +738,21 @@ __global__ void __launch_bounds__(wp::kThreads, 1)
             mbar_init(smem_u32(&sh.item_empty[i]), kItemConsumers);
         }
         mbar_init(smem_u32(&sh.q_full), 1);
-        mbar_init(smem_u32(&sh.q_empty), 1);
-        mbar_init(smem_u32(&sh.drain), 1);
+        mbar_init(smem_u32(&sh.q_empty), kTiles);
         mbar_init(smem_u32(&sh.next_full), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&sh.kv_full[i]), 1);
-            mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+            mbar_init(smem_u32(&sh.kv_empty[i]), kTiles);
         }
         for (int t = 0; t < kTiles; ++t) {
-            mbar_init(smem_u32(&sh.s_full[t]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), 4);   // one arrival per softmax warp
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&sh.s_full[t][i]), 1);
+                mbar_init(smem_u32(&sh.p_full[t][i]), 4);  // one arrival per softmax warp
+            }
+            mbar_init(smem_u32(&sh.o_mid[t]), 1);
             mbar_init(smem_u32(&sh.o_full[t]), 1);
             mbar_init(smem_u32(&sh.o_empty[t]), 4);
+            mbar_init(smem_u32(&sh.drain[t]), 1);
         }
         sh.abort = 0;
         fence_mbar_init();
@@ -731,9 +781,9 @@ __global__ void __launch_bounds__(wp::kThreads, 1)
     if (warp == kLoadWarp) {
         load_role<D>(&tm_q, &tm_k, &tm_v, p, sh, sbase, lane);
     } else if (warp == kMmaWarp) {
-        if (lane == 0)
-            mma_role<D, kBf16>(p, sh, sbase);
-        __syncwarp();
+        mma_role<D, kBf16, 0>(p, sh, sbase);
+    } else if (warp == kMmaWarp + 1) {
+        mma_role<D, kBf16, 1>(p, sh, sbase);
     } else {
         softmax_role<D, kBf16>(p, sh, smem, warp, lane);
     }

@@ -53,6 +53,9 @@ def _check(paged, q, out, news, window, sinks, scale, seqs=None):
     ([400, 333], [400, 100], 40, 2, 64, 16, 5000, 0),
     ([2048], [2048], 2, 2, 128, 16, 1000, 0),
     ([2048], [1000], 10, 2, 64, 32, 511, 700),
+    ([1000, 190, 641], [300, 5, 64], 4, 2, 128, 16, 3, 200),
+    ([1000, 640], [33, 200], 8, 1, 64, 32, 40, 400),
+    ([900, 321], [260, 130], 1, 1, 64, 8, 65, 10),
     ([9] * 70, [k % 10 for k in range(70)], 2, 1, 128, 8, 4, 2),
 ])
 def test_against_64_bits(dtype, lens, news, heads, kvh, d, bs, window, sinks):
