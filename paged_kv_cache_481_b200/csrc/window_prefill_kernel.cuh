@@ -85,7 +85,7 @@ constexpr int kThreads = (kMmaWarp + kTiles) * 32;
 constexpr uint32_t kTmemCols = 512, kTmemO = 2 * kN;
 constexpr float kRescaleLog2 = 8.0f;  // move the reference only past this growth
 constexpr float kShift = 7.0f;        // weights are 2^7 times the softmax's
-constexpr int kPolyEvery = 4;         // pairs of weights, of which one is a polynomial
+constexpr int kPolyEvery = 8;         // pairs of weights, of which one is a polynomial
 constexpr float kFloor = -1e30f;      // reference of a row that has seen nothing yet
 
 template <int D>
@@ -109,7 +109,7 @@ struct Item {
     int tiles;                 // context tiles of the walk; 0: no more items
 
     // Context tile j of the walk: the window's first, the first tokens', the rest.
-    __device__ __forceinline__ int tile(int j) const
+    static __device__ __forceinline__ int tile(int j, int first, int sink_tiles)
     {
         return j == 0 ? first : j <= sink_tiles ? j - 1 : first + j - sink_tiles;
     }
@@ -323,7 +323,7 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
         const int32_t *trow = p.tables + size_t(it.b) * p.max_blocks;
         for (int j = 0; go && j < it.tiles; ++j) {
             // one run of up to a block per lane
-            const int tok = it.tile(j) * kN + lane * box;
+            const int tok = Item::tile(j, it.first, it.sink_tiles) * kN + lane * box;
             const bool seen = lane * box < kN && tok < it.L && (tok + box > it.lo || tok < p.sinks);
             bool ok_id = false;
             int y = 0;
@@ -451,8 +451,9 @@ __device__ __forceinline__ void mma_role(const WindowPrefillParams &p, Shared &s
         ok = wait(sh.q_full, u) && scores(0);
         for (int y = 0; ok && y < 2 * tiles; ++y) {
             const int iv = ring + (y & ~1) + 1;
+            const bool mine = y >= begin && y < end;
             ok = (y + 1 >= 2 * tiles || scores(y + 1)) && ((y & 1) || wait(sh.kv_full[iv % kRing], iv / kRing));
-            if (ok && y >= begin && y < end) {
+            if (ok && mine) {
                 // the previous item's epilogue has read O, the softmax has written P
                 const int x = pv_cnt++;
                 ok = (y > begin || items == 0 || wait(sh.o_empty[t], items - 1)) &&
@@ -531,32 +532,41 @@ __device__ __forceinline__ uint64_t exp2_poly_f32x2(uint64_t x)
     return uint64_t(lo) | uint64_t(hi) << 32;
 }
 
-// P = 2^(c * s - m) of the row, as 16-bit pairs over the first 32 columns of
-// its buffer; returns the row sum of the unrounded P.  One pair in kPolyEvery
-// goes through the polynomial, which takes that share off the special-function
-// unit (4 lanes a clock and quarter of an SM).
+// P = 2^(c * s - m) of the row as 16-bit pairs over the first 32 columns of its
+// buffer; also the row sum of the unrounded P and the row maximum of s, which
+// nothing here waits for.  One pair in kPolyEvery goes through the polynomial,
+// which takes that share off the special-function unit (4 lanes a clock and
+// quarter of an SM).
 template <bool kBf16>
-__device__ __forceinline__ float write_weights(uint32_t tS, const uint32_t (&r)[kHalf], float c, float m)
+__device__ __forceinline__ void write_weights(uint32_t tS, const uint32_t (&r)[kHalf], float c, float m,
+                                              float &sum, float &largest)
 {
     const uint64_t cc = pack_f32x2(c, c), mm = pack_f32x2(-m, -m);
-    uint64_t sum[2] = {0, 0};
-    uint32_t pk[kHalf / 2];
+    uint64_t total[2] = {0, 0};
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < kHalf / 2; ++e) {
-        uint64_t x = fma_f32x2(uint64_t(r[2 * e]) | uint64_t(r[2 * e + 1]) << 32, cc, mm);
-        if (kPolyEvery > 0 && e % kPolyEvery == kPolyEvery - 1) {
-            x = exp2_poly_f32x2(x);
-        } else {
+    for (int part = 0; part < 2; ++part) {
+        uint32_t pk[kHalf / 4];
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i) {
+            const int e = part * (kHalf / 4) + i;
+            uint64_t x = fma_f32x2(uint64_t(r[2 * e]) | uint64_t(r[2 * e + 1]) << 32, cc, mm);
+            if (kPolyEvery > 0 && e % kPolyEvery == kPolyEvery - 1) {
+                x = exp2_poly_f32x2(x);
+            } else {
+                const float2 v = unpack_f32x2(x);
+                x = pack_f32x2(exp2_sfu(v.x), exp2_sfu(v.y));
+            }
+            total[e & 1] = add_f32x2(total[e & 1], x);
             const float2 v = unpack_f32x2(x);
-            x = pack_f32x2(exp2_sfu(v.x), exp2_sfu(v.y));
+            pk[i] = Half16<kBf16>::pack(v.x, v.y);
+            top[e & 1] = max3f(top[e & 1], __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
-        sum[e & 1] = add_f32x2(sum[e & 1], x);
-        const float2 v = unpack_f32x2(x);
-        pk[e] = Half16<kBf16>::pack(v.x, v.y);
+        tmem_store16(tS + uint32_t(part * (kHalf / 4)), pk);
     }
-    tmem_store32(tS, pk);
-    const float2 v = unpack_f32x2(add_f32x2(sum[0], sum[1]));
-    return v.x + v.y;
+    const float2 v = unpack_f32x2(add_f32x2(total[0], total[1]));
+    sum = v.x + v.y;
+    largest = fmaxf(top[0], top[1]);
 }
 
 template <int D, bool kBf16>
@@ -578,20 +588,24 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
         if (!__all_sync(kFullMask, wait_or_abort(smem_u32(&sh.item_full[slot]),
                                                  uint32_t(u / kItemRing) & 1u, abort, p.err)))
             break;
-        const Item it = sh.item[slot];
+        // (field by field: a copy would lie in local memory)
+        const Item &it = sh.item[slot];
+        const int tiles = it.tiles, first = it.first, sink_tiles = it.sink_tiles, L = it.L, lo = it.lo;
+        const int head = it.h * p.group + r_head, token = it.token + t * p.tq + r_token;
+        const int rows = it.rows[t], my_pos = it.pos0[t] + r_token, begin = it.begin[t], end = it.end[t];
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_u32(&sh.item_empty[slot]));
-        if (it.tiles == 0)
+        if (tiles == 0)
             break;
         const int item_ring = ring;
-        ring += 2 * it.tiles;
-        if (it.rows[t] <= 0)
+        ring += 2 * tiles;
+        if (rows <= 0)
             continue;
-        const bool live = (warp & 3) * 32 < it.rows[t] * p.group;  // the warp holds rows
-        const int my_pos = it.pos0[t] + r_token;
-        const int my_lo = max(0, my_pos - p.window + 1), my_end = min(my_pos + 1, it.L);
-        const int begin = it.begin[t], end = it.end[t];
+        const bool live = (warp & 3) * 32 < rows * p.group;  // the warp holds rows
+        const int my_lo = max(0, my_pos - p.window + 1), my_end = min(my_pos + 1, L);
+        // no row of the warp needs a mask for tokens in [warp_lo, warp_end)
+        const int warp_lo = __reduce_max_sync(kFullMask, my_lo), warp_end = __reduce_min_sync(kFullMask, my_end);
         float m_ref = kFloor, l = 0.f;
         bool ok = true;
         for (int y = begin; y < end; ++y) {
@@ -601,22 +615,28 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
             if (!ok)
                 break;
             tc_fence_after_sync();
-            const int t0 = it.tile(y >> 1) * kN + (y & 1) * kHalf;
+            const int t0 = Item::tile(y >> 1, first, sink_tiles) * kN + (y & 1) * kHalf;
             if (live) {
                 uint32_t row[kHalf];
                 tmem_load32_into(tS + uint32_t(buf) * kHalf, row);
                 tmem_load32_into(tS + uint32_t(buf) * kHalf + 32u, row + 32);
                 tmem_wait_ld();
-                const int lo = my_lo - t0, lim = my_end - t0, sinks = p.sinks - t0;
-                if (__any_sync(kFullMask, lim < kHalf || (lo > 0 && sinks < kHalf)))
-                    mask_row(row, lo, lim, sinks);
-                const float m_new = fmaxf(m_ref, row_max(row) * c);
-                if (y == begin) {
-                    m_ref = m_new;
-                } else if (__any_sync(kFullMask, m_new > m_ref + kRescaleLog2)) {
-                    // move this warp's reference: rescale O and l,
-                    // once the last step's product is done, which the next
-                    // scores or the end of the item tell
+                if (t0 + kHalf > warp_end || (t0 < warp_lo && t0 + kHalf > p.sinks))
+                    mask_row(row, my_lo - t0, my_end - t0, p.sinks - t0);
+                if (y == begin)
+                    m_ref = fmaxf(m_ref, row_max(row) * c);
+                // The weights are taken against the reference as it is; where a
+                // score turns out to be too far above it, which is rare, it is
+                // moved and they are taken again.
+                float sum, largest;
+                for (;;) {
+                    write_weights<kBf16>(tS + uint32_t(buf) * kHalf, row, c, m_ref - kShift, sum, largest);
+                    const float m_new = fmaxf(m_ref, largest * c);
+                    if (!__any_sync(kFullMask, m_new > m_ref + kRescaleLog2))
+                        break;
+                    // move this warp's reference: rescale O and l, once the
+                    // last step's product is done, which the next scores or
+                    // the end of the item tell
                     ok = __all_sync(kFullMask,
                                     y + 1 < end
                                         ? wait_or_abort(smem_u32(&sh.s_full[t][buf ^ 1]),
@@ -640,21 +660,23 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
                     l *= alpha;
                     m_ref = m_new;
                 }
-                l += write_weights<kBf16>(tS + uint32_t(buf) * kHalf, row, c, m_ref - kShift);
+                if (!ok)
+                    break;
+                l += sum;
                 tmem_wait_st();
             }
             // V rows that no row of the item sees (behind the context, before
             // the window, stale ring contents) are zeroed, so that 0 * garbage
             // cannot reach O: by each tile that takes part in the step, since
             // either may be first, two threads a row.
-            if (t0 + kHalf > it.L || (t0 < it.lo && t0 + kHalf > p.sinks)) {
+            if (t0 + kHalf > L || (t0 < lo && t0 + kHalf > p.sinks)) {
                 const int iv = item_ring + (y & ~1) + 1;
                 ok = __all_sync(kFullMask, wait_or_abort(smem_u32(&sh.kv_full[iv % kRing]),
                                                          uint32_t(iv / kRing) & 1u, abort, p.err));
                 if (!ok)
                     break;
                 const int vr = r >> 1, tok = t0 + vr;
-                if (!(tok < it.L && (tok >= it.lo || tok < p.sinks))) {
+                if (!(tok < L && (tok >= lo || tok < p.sinks))) {
                     unsigned char *at = smem + S::kOffRing + uint32_t(iv % kRing) * S::kTileBytes +
                                         uint32_t(y & 1) * (S::kTileBytes / 2) +
                                         uint32_t(vr >> 3) * S::kGroupBytes + uint32_t(vr & 7) * 128u;
@@ -684,10 +706,9 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
         if (live) {
             tc_fence_after_sync();
             const float inv = 1.f / l;
-            const bool store = r < it.rows[t] * p.group;
-            const size_t token = size_t(it.token) + t * p.tq + r_token;
-            uint4 *dst = reinterpret_cast<uint4 *>(
-                static_cast<uint16_t *>(p.out) + (token * p.heads + it.h * p.group + r_head) * D);
+            const bool store = r < rows * p.group;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
+                                                   (size_t(token) * p.heads + head) * D);
 #pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
                 uint32_t o[32];
