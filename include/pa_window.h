@@ -63,8 +63,8 @@ typedef enum pa_kv8_type {
  * or (2j, 2j + 1) when `interleaved` is not 0; the other dims are copied.
  * q's rotated rows go to q_out (which may be q itself, with the same stride),
  * key's to k_cache and value's unrotated rows to v_cache at the token's slot.
- * A token with a negative slot is padding: nothing of it is read or written,
- * its q_out row included.
+ * A token with a negative slot is padding: nothing of it is written, its q_out
+ * row included.
  *   cos_sin    [max_position, rotary_dim] float: the cosines of the
  *              rotary_dim / 2 angles, then their sines
  *   positions  [num_tokens] int64
@@ -72,7 +72,8 @@ typedef enum pa_kv8_type {
  *              of 8, at least heads * head_dim), so that q, key and value may
  *              be parts of one projection's output
  * rotary_dim is a multiple of 16 in [0, head_dim] (else PA_ERR_UNSUPPORTED);
- * 0 rotates nothing and cos_sin and positions may be NULL.  The arithmetic is
+ * 0 rotates nothing and cos_sin and positions may be NULL (else max_position
+ * is at least 1).  The arithmetic is
  * in fp32, each product and sum rounded by itself, then rounded once to the
  * 16-bit type.  A slot outside the pool or a position outside the table is
  * recorded (PA_DEVERR_SLOT, PA_DEVERR_POSITION) and the token skipped.  Slots
@@ -116,12 +117,13 @@ PA_API pa_status pa_rope_and_cache_q8(void *q_out, int64_t q_out_stride, const v
 
 /*
  * Bytes of workspace pa_decode_window and pa_decode_q8 need: partial results
- * of the contexts that are split between blocks of threads, and one merge
- * counter per (sequence, K/V head, 16 query heads); the same for every
- * head_dim.  Never 0.  Zero it once
- * before its first use (pa_decode_workspace_init); every completed call
- * leaves it ready for the next, of any size that fits it.  Calls that share a
- * workspace must not overlap on the GPU (this holds for replayed graphs too).
+ * of the contexts that are split between blocks of threads (34 MB), and one
+ * merge counter per (sequence, K/V head, 8 or 16 query heads); the same for
+ * every head_dim.  Never 0.  Zero it once before its first use
+ * (pa_decode_workspace_init); every completed call leaves it ready for the
+ * next, of any size that fits it (after PA_DEVERR_TIMEOUT, zero it again).
+ * Calls that share a workspace must not overlap on the GPU (this holds for
+ * replayed graphs too).
  */
 PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                               int head_dim);
@@ -132,8 +134,8 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
  *     out[b, h, :] = sum_t exp(s_t - max s) V_t / sum_t exp(s_t - max s),
  *     s_t = scale * sum_d q[b, h, d] * K_t[d],  over the positions t it sees.
  * Scores, softmax statistics and sums are fp32; the weights enter the product
- * with V in the cache's 16-bit type.  L == 0 writes zeros.  Positions that
- * are not seen are never read, whatever they hold.  max_context_len bounds
+ * with V in the cache's 16-bit type.  L == 0 writes zeros.  What positions
+ * that are not seen hold has no effect.  max_context_len bounds
  * context_lens and must not exceed max_blocks_per_seq * block_size or 2^30.  Results
  * do not depend on the order in which blocks of threads run.
  */

@@ -31,7 +31,7 @@ pa_status rope_params(pa::RopeParams &p, void *q_out, int64_t q_out_stride, cons
         return PA_OK;
     const int64_t q_row = int64_t(num_heads) * head_dim, kv_row = int64_t(num_kv_heads) * head_dim;
     if (!q_out || !q || !key || !value || !k_cache || !v_cache || !slot_mapping ||
-        (rotary_dim > 0 && (!cos_sin || !positions)))
+        (rotary_dim > 0 && (!cos_sin || !positions || max_position < 1)))
         return PA_ERR_INVALID_ARG;
     if (!aligned16(q_out) || !aligned16(q) || !aligned16(key) || !aligned16(value) ||
         !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(cos_sin) ||

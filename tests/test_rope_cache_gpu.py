@@ -239,3 +239,68 @@ def test_many_tokens_of_one_call_and_a_replayed_graph():
     bound = s / 2 * (1 + 2.0 ** -20) + 2.0 ** -20 * ref.abs() + 4 * 2.0 ** -24 * mag
     assert bool(((got - ref).abs() <= bound).all())
     assert bool((scales[:, kvh] == 0).all())      # the padding head's scales are not written
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_codes_of_extreme_magnitudes(kind):
+    """Rows near both ends of bf16's range: the quotient by the scale neither
+    overflows nor loses its last bits."""
+    code_type, top = CODES[kind]
+    kvh, d, bs = 1, 64, 8
+    base = _rand((4, kvh, d), torch.float32, 31)
+    for factor in (2.0 ** 120, 2.0 ** 100, 1.0, 2.0 ** -100, 2.0 ** -117):
+        x = (base * factor).to(BF16)
+        kc, vc = (torch.zeros((1, kvh, bs, d), device="cuda").to(code_type) for _ in "kv")
+        scales = torch.zeros((1, 2, 2), device="cuda")
+        slots = torch.arange(4, device="cuda")
+        binding.pa_rope_and_cache_q8(torch.empty_like(x), x, x, x, kc, vc, scales, None, None, slots)
+        m = x.double().abs().amax()
+        want = x.double() * top / m                 # in codes
+        got = kc[0, 0, :4].float().double()
+        step = torch.full_like(want, 0.5) if kind == "int8" else torch.maximum(
+            2.0 ** -4 * want.abs(), torch.full_like(want, 2.0 ** -10))
+        assert bool(((got - want[:, 0]).abs() <= step[:, 0] * (1 + 2.0 ** -20)).all())
+        # the scale is m / top rounded once (subnormal ones to 2^-149)
+        assert abs(float(scales[0, 0, 0].double() - m / top)) <= max(2.0 ** -24 * float(m / top),
+                                                                     2.0 ** -150)
+
+
+def test_ties_follow_the_exact_quotient():
+    """bf16 values whose x top / m lies exactly between two e4m3 numbers go to
+    the even one, though the scale itself is rounded."""
+    d, top = 64, 448.0
+    x = torch.zeros((1, 1, d), dtype=BF16, device="cuda")
+    x[0, 0, 0] = 7.0 * 1.375                        # m: s = m / 448 is not a power of two
+    m = float(x[0, 0, 0])
+    want = []
+    for i in range(1, d):
+        # v 448 / m = 17/16 * 2^k or 19/16 * 2^k: between neighbours of step 1/8
+        v = (17.0 if i % 2 else 19.0) / 16.0 * 2.0 ** (i % 5) * m / 448.0
+        x[0, 0, i] = v
+        got = float(x[0, 0, i]) * 448.0 / m
+        want.append(got)
+    kc, vc = (torch.zeros((1, 1, 8, d), device="cuda").to(torch.float8_e4m3fn) for _ in "kv")
+    scales = torch.zeros((1, 2, 2), device="cuda")
+    binding.pa_rope_and_cache_q8(torch.empty_like(x), x, x, x, kc, vc, scales, None, None,
+                                 torch.zeros(1, dtype=torch.int64, device="cuda"))
+    exact = torch.tensor(want, dtype=torch.float64).float().to(torch.float8_e4m3fn).float()
+    assert torch.equal(vc[0, 0, 0, 1:].float().cpu(), exact)
+
+
+def test_tensors_of_another_device_or_layout_are_refused():
+    x = _rand((2, 1, 64), F16, 1)
+    kc, vc = (torch.zeros((1, 1, 8, 64), dtype=F16, device="cuda") for _ in "kv")
+    slots = torch.tensor([0, 1], device="cuda")
+    call = lambda *a: binding.pa_rope_and_cache(*a, None, None, slots)
+    with pytest.raises(ValueError):
+        call(x, x.cpu(), x, x, kc, vc)
+    with pytest.raises(ValueError):
+        call(x, x, x, x, kc.cpu(), vc)
+    with pytest.raises(ValueError):      # heads that do not lie side by side
+        wide = _rand((2, 2, 64), F16, 1)[:, :, :].transpose(0, 1)
+        binding.pa_rope_and_cache(wide.contiguous(), wide, x, x, kc, vc, None, None, slots)
+    with pytest.raises(AssertionError):
+        call(x, x, x.to(BF16), x, kc, vc)
+    with pytest.raises(binding.PAError):  # a token stride that is not a multiple of 8
+        odd = torch.zeros((2, 68), dtype=F16, device="cuda")[:, :64].unsqueeze(1)
+        call(odd, odd, x, x, kc, vc)

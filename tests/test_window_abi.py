@@ -37,7 +37,7 @@ def test_rope_refuses(lib, eight):
     for c in (dict(n=-1), dict(nb=0), dict(maxp=-1), dict(dtype=2), dict(dtype=-1), dict(h=3),
               dict(kvh=0), dict(h=0), dict(h=512, kvh=2), dict(q=NULL), dict(q_out=NULL),
               dict(k=NULL), dict(v=NULL), dict(kc=NULL), dict(vc=NULL), dict(slots=NULL),
-              dict(table=NULL), dict(pos=NULL), dict(q=ODD), dict(kc=ODD), dict(table=ODD),
+              dict(table=NULL), dict(pos=NULL), dict(maxp=0), dict(q=ODD), dict(kc=ODD), dict(table=ODD),
               dict(qs=248), dict(ks=120), dict(vs=0), dict(qo=260), dict(ks=-128),
               dict(qs=264)):           # q in place with another stride
         assert r(**c) == INVALID, c
