@@ -111,6 +111,21 @@ __device__ __forceinline__ void tmem_load16_async(uint32_t taddr, uint32_t (&r)[
         : "memory");
 }
 
+// 16 lanes x 32 columns in the layout of matrix fragments: of every 8 columns,
+// r[4 i], r[4 i + 1] are columns 2 (lane % 4), + 1 of row lane / 4, r[4 i + 2],
+// r[4 i + 3] the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_load_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Store 16 / 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
 {

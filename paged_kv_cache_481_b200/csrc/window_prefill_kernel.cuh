@@ -569,6 +569,25 @@ __device__ __forceinline__ void write_weights(uint32_t tS, const uint32_t (&r)[k
     largest = fmaxf(top[0], top[1]);
 }
 
+__device__ __forceinline__ uint16_t *shfl_pointer(uint16_t *v, int lane)
+{
+    return reinterpret_cast<uint16_t *>(__shfl_sync(kFullMask, reinterpret_cast<unsigned long long>(v), lane));
+}
+
+// Word i of four lanes (c = 0 .. 3) becomes the words of lane i, in order.
+__device__ __forceinline__ uint4 transpose_quad(const uint32_t (&w)[4], int c)
+{
+    // with the neighbour: two words of column c & 1, two of 2 + (c & 1)
+    const bool odd = c & 1, upper = c & 2;
+    const uint32_t x = __shfl_xor_sync(kFullMask, odd ? w[0] : w[1], 1);
+    const uint32_t y = __shfl_xor_sync(kFullMask, odd ? w[2] : w[3], 1);
+    const uint32_t a0 = odd ? x : w[0], a1 = odd ? w[1] : x, b0 = odd ? y : w[2], b1 = odd ? w[3] : y;
+    // with the other pair
+    const uint32_t u = __shfl_xor_sync(kFullMask, upper ? a0 : b0, 2);
+    const uint32_t v = __shfl_xor_sync(kFullMask, upper ? a1 : b1, 2);
+    return upper ? make_uint4(u, v, b0, b1) : make_uint4(a0, a1, u, v);
+}
+
 template <int D, bool kBf16>
 __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Shared &sh,
                                              unsigned char *smem, int warp, int lane)
@@ -705,25 +724,37 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
         ++items;
         if (live) {
             tc_fence_after_sync();
+            // O comes in the layout of a matrix fragment (lane: row lane / 4 of 8,
+            // two columns of every eight); the four lanes of a row exchange
+            // until each holds 16 bytes, so that a store covers 64 bytes of 8
+            // rows instead of 16 bytes of 32.
             const float inv = 1.f / l;
-            const bool store = r < rows * p.group;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                                   (size_t(token) * p.heads + head) * D);
+            uint16_t *my_dst = r < rows * p.group ? static_cast<uint16_t *>(p.out) +
+                                                        (size_t(token) * p.heads + head) * D
+                                                  : nullptr;
+            const int g = lane >> 2, c4 = lane & 3;
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                tmem_load32_async(tO + uint32_t(cc * 32), o);
-                tmem_wait_ld();
-                if (store) {
+            for (int part = 0; part < 2; ++part) {  // rows 16 part .. 16 part + 15 of the warp
+                const float inv0 = __shfl_sync(kFullMask, inv, 16 * part + g);
+                const float inv1 = __shfl_sync(kFullMask, inv, 16 * part + g + 8);
+                uint16_t *dst0 = shfl_pointer(my_dst, 16 * part + g), *dst1 = shfl_pointer(my_dst, 16 * part + g + 8);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t v[4];
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[16], w[2][4];
+                    tmem_load_16x256b_x4(tO + (uint32_t(16 * part) << 16) + uint32_t(cc * 32), o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = Half16<kBf16>::pack(__uint_as_float(o[g * 8 + 2 * e]) * inv,
-                                                       __uint_as_float(o[g * 8 + 2 * e + 1]) * inv);
-                        dst[cc * 4 + g] = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        w[0][i] = Half16<kBf16>::pack(__uint_as_float(o[4 * i]) * inv0,
+                                                      __uint_as_float(o[4 * i + 1]) * inv0);
+                        w[1][i] = Half16<kBf16>::pack(__uint_as_float(o[4 * i + 2]) * inv1,
+                                                      __uint_as_float(o[4 * i + 3]) * inv1);
                     }
+                    const uint4 v0 = transpose_quad(w[0], c4), v1 = transpose_quad(w[1], c4);
+                    if (dst0)
+                        *reinterpret_cast<uint4 *>(dst0 + cc * 32 + c4 * 8) = v0;
+                    if (dst1)
+                        *reinterpret_cast<uint4 *>(dst1 + cc * 32 + c4 * 8) = v1;
                 }
             }
             tc_fence_before_sync();
