@@ -22,6 +22,17 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
+// Two 16 x 16 matrices of bytes, transposed: lane i gives the address of row
+// i % 16 of matrix i / 16; lane (g, c) gets rows 4c .. 4c + 3 of columns g and
+// g + 8 of each.
+__device__ __forceinline__ void ldmatrix_x2_trans8(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // Transpose an 8 x 8 matrix of 16-bit values (row i: lanes 4 i .. 4 i + 3).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v)
 {
@@ -42,13 +53,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr)
                  : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 

@@ -122,16 +122,12 @@ struct WindowTraits {
         }
     }
 
-    // Token of product row g (+ 8 when `high`) within 16 tokens: an order in
-    // which the 8-bit rows' loads have no bank conflicts.
+    // Token of product row g (+ 8 when `high`) within 16 tokens: for 8-bit
+    // rows in the order in which the transposing load gives V, four tokens to
+    // a lane.
     static __device__ __forceinline__ int token_of(int g, int high)
     {
-        if constexpr (!kEight)
-            return g + 8 * high;
-        else if constexpr (D == 128)
-            return ((g & 1) ? (g - 1) ^ 5 : g) + 8 * high;
-        else
-            return 4 * (g >> 1) + (g & 1) + 2 * high;
+        return kEight ? 4 * (g >> 1) + (g & 1) + 2 * high : g + 8 * high;
     }
 };
 
@@ -244,10 +240,10 @@ template <bool kE4m3>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
     if constexpr (kE4m3) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3);
-        lo = uint32_t(a.x) | (uint32_t(a.y) << 16);
-        hi = uint32_t(b.x) | (uint32_t(b.y) << 16);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
         // a byte under the exponent of 1024 is the number 1024 + byte; with
         // the sign bit flipped the byte is code + 128
@@ -826,33 +822,23 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                             mma16816<W::kBf16>(o[nq][n], a, pb[nq][0], pb[nq][1]);
                     }
                 } else {
-                    // codes of dims [g D/8, (g + 1) D/8) of the four tokens of
-                    // the lane's columns; pairs of tokens interleaved bytewise
-                    constexpr int kWords = D / 32;
-                    uint32_t w[4][kWords];
+                    // lane (g, c): codes of tokens 4c .. 4c + 3 of dims g and g + 8
+                    // of 16-dim chunks 2n, 2n + 1
+                    const int row = 16 * mt + (lane & 15), high = lane >> 4;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 16 * mt + W::token_of(2 * c + (e & 1), e >> 1);
-                        if constexpr (D == 128) {
-                            const uint4 x = lds128(vt + W::at(row, g));
-                            w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
-                        } else {
-                            const uint2 x = lds64(vt + W::at(row, g >> 1) + uint32_t(g & 1) * 8u);
-                            w[e][0] = x.x, w[e][1] = x.y;
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < kWords; ++n)
+                    for (int n = 0; n < kDt / 2; ++n) {
+                        uint32_t w[4];
+                        ldmatrix_x2_trans8(vt + W::at(row, 2 * n + high), w);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t order = e ? 0x7362 : 0x5140;
                             uint32_t a[4];
-                            widen4<kE4m3>(__byte_perm(w[0][n], w[1][n], order), a[0], a[1]);
-                            widen4<kE4m3>(__byte_perm(w[2][n], w[3][n], order), a[2], a[3]);
+                            widen4<kE4m3>(w[2 * e], a[0], a[2]);
+                            widen4<kE4m3>(w[2 * e + 1], a[1], a[3]);
 #pragma unroll
                             for (int nq = 0; nq < kNq; ++nq)
                                 mma16816<false>(o[nq][2 * n + e], a, pb[nq][0], pb[nq][1]);
                         }
+                    }
                 }
             }
             __syncwarp();  // the stage may be filled again
@@ -886,15 +872,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             hi2 = movmatrix_trans(hi2);
             if (8 * nq + g < rows) {
                 uint16_t *dst = static_cast<uint16_t *>(p.out) + (out_row + 8 * nq + g) * D;
-                if constexpr (!kEight) {
-                    *reinterpret_cast<uint32_t *>(dst + 16 * n + 2 * c) = lo2;
-                    *reinterpret_cast<uint32_t *>(dst + 16 * n + 8 + 2 * c) = hi2;
-                } else {
-                    *reinterpret_cast<uint32_t *>(dst + (D / 8) * (2 * c) + 2 * n) =
-                        __byte_perm(lo2, hi2, 0x5410);
-                    *reinterpret_cast<uint32_t *>(dst + (D / 8) * (2 * c + 1) + 2 * n) =
-                        __byte_perm(lo2, hi2, 0x7632);
-                }
+                *reinterpret_cast<uint32_t *>(dst + 16 * n + 2 * c) = lo2;
+                *reinterpret_cast<uint32_t *>(dst + 16 * n + 8 + 2 * c) = hi2;
             }
         };
         // Parts of the unit, and their slots.  With ranges, the parts lie
