@@ -321,20 +321,23 @@ __device__ __forceinline__ void load_role(const CUtensorMap *tm_q, const CUtenso
             break;
         ++items;
         const int32_t *trow = p.tables + size_t(it.b) * p.max_blocks;
-        for (int j = 0; go && j < it.tiles; ++j) {
-            // one run of up to a block per lane
+        // one run of up to a block per lane; the ids of the next tile's blocks
+        // are on their way while this one's boxes wait for their places
+        auto look_up = [&](int j) {
             const int tok = Item::tile(j, it.first, it.sink_tiles) * kN + lane * box;
-            const bool seen = lane * box < kN && tok < it.L && (tok + box > it.lo || tok < p.sinks);
-            bool ok_id = false;
-            int y = 0;
-            if (seen) {
-                const int id = trow[tok >> p.log2_bs];
-                ok_id = unsigned(id) < unsigned(p.num_blocks);
-                if (!ok_id)
-                    atomicOr(p.err, PA_DEVERR_BLOCK_ID);
-                // in groups of 8 rows
-                y = ok_id ? int((((long long)id * p.kv_heads + it.h) * bs + (tok & (bs - 1))) >> 3) : 0;
-            }
+            const bool seen = j < it.tiles && lane * box < kN && tok < it.L && (tok + box > it.lo || tok < p.sinks);
+            return seen ? trow[tok >> p.log2_bs] : -2;  // -2: nothing of the run is seen
+        };
+        int ahead = look_up(0);
+        for (int j = 0; go && j < it.tiles; ++j) {
+            const int id = ahead;
+            ahead = look_up(j + 1);
+            const bool ok_id = unsigned(id) < unsigned(p.num_blocks);
+            if (id != -2 && !ok_id)
+                atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+            // in groups of 8 rows
+            const int in_block = (Item::tile(j, it.first, it.sink_tiles) * kN + lane * box) & (bs - 1);
+            const int y = ok_id ? int((((long long)id * p.kv_heads + it.h) * bs + in_block) >> 3) : 0;
             const uint32_t bytes = uint32_t(__popc(__ballot_sync(kFullMask, ok_id))) * uint32_t(box) *
                                    uint32_t(D * 2);
 #pragma unroll
