@@ -472,9 +472,9 @@ _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _KV8_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 
-def _raw_stream(stream) -> int:
+def _raw_stream(stream, device: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -486,16 +486,15 @@ def _pointers(device: int, *tensors):
     return [t.data_ptr() for t in tensors]
 
 
-def _rows(device: int, *tensors):
-    """Addresses and elements between tokens of [tokens, heads, head_dim] rows
-    that may be slices of wider rows."""
+def _rows(device: int, n: int, d: int, *rows):
+    """Addresses and elements between tokens of (tensor, heads) pairs of
+    [n, heads, d] rows that may be slices of wider rows."""
     out = []
-    for t in tensors:
-        n, h, d = t.shape
+    for t, h in rows:
         if t.get_device() != device:
             _ptr(t)
         step, head, one = t.stride()
-        if (d > 1 and one != 1) or (h > 1 and head != d):
+        if (one != 1 and d > 1) or (head != d and h > 1):
             raise ValueError("libpa takes token rows whose heads are contiguous")
         out += (t.data_ptr(), step if n > 1 else h * d)
     return out
@@ -504,24 +503,25 @@ def _rows(device: int, *tensors):
 def _rope_args(q_out, q, key, value, k_cache, v_cache, scales, cos_sin, positions, slot_mapping,
                interleaved):
     """Checks and the arguments that both rotating writes share."""
-    n, h, d = q.shape
+    shape, dtype = q.shape, q.dtype
+    n, h, d = shape
     nb, kvh, bs, dk = k_cache.shape
-    dtype = q.dtype
     assert dtype in _DTYPES and dtype == q_out.dtype == key.dtype == value.dtype
-    assert q_out.shape == q.shape and key.shape == value.shape == (n, kvh, d) and dk == d
+    assert q_out.shape == shape and key.shape == value.shape == (n, kvh, d) and dk == d
     assert v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
     assert slot_mapping.dtype == torch.int64 and slot_mapping.numel() == n
     device = torch.cuda.current_device()
     if cos_sin is None:
-        table = [0, 0, 0, int(interleaved), 0]
+        table = (0, 0, 0, int(interleaved), 0)
     else:
         max_position, rotary = cos_sin.shape
         assert cos_sin.dtype == torch.float32
         assert positions.dtype == torch.int64 and positions.numel() == n
         cos_sin, positions = _pointers(device, cos_sin, positions)
-        table = [cos_sin, rotary, max_position, int(interleaved), positions if rotary else 0]
-    return [*_rows(device, q_out, q, key, value), *_pointers(device, k_cache, v_cache, *scales), *table,
-            *_pointers(device, slot_mapping), n, h, kvh, d, bs, nb, _DTYPES[dtype]]
+        table = (cos_sin, rotary, max_position, int(interleaved), positions if rotary else 0)
+    return device, [*_rows(device, n, d, (q_out, h), (q, h), (key, kvh), (value, kvh)),
+                    *_pointers(device, k_cache, v_cache, *scales), *table,
+                    *_pointers(device, slot_mapping), n, h, kvh, d, bs, nb, _DTYPES[dtype]]
 
 
 def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping,
@@ -531,9 +531,9 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, cos_sin, positions
     [max_position, rotary_dim] fp32 holds cosines, then sines (None: no
     rotation).  q, key and value may be slices of one projection's output."""
     assert k_cache.dtype == q.dtype
-    args = _rope_args(q_out, q, key, value, k_cache, v_cache, (), cos_sin, positions, slot_mapping,
-                      interleaved)
-    _check((_lib or load()).pa_rope_and_cache(*args, _raw_stream(stream)), "pa_rope_and_cache")
+    device, args = _rope_args(q_out, q, key, value, k_cache, v_cache, (), cos_sin, positions,
+                              slot_mapping, interleaved)
+    _check((_lib or load()).pa_rope_and_cache(*args, _raw_stream(stream, device)), "pa_rope_and_cache")
 
 
 def _check_scales(kv_scales, k_codes, v_codes):
@@ -549,10 +549,10 @@ def pa_rope_and_cache_q8(q_out, q, key, value, k_codes, v_codes, kv_scales, cos_
     with one scale per block and head, kv_scales [num_blocks, num_kv_heads
     rounded up to even, 2] fp32."""
     _check_scales(kv_scales, k_codes, v_codes)
-    args = _rope_args(q_out, q, key, value, k_codes, v_codes, (kv_scales,), cos_sin, positions,
-                      slot_mapping, interleaved)
+    device, args = _rope_args(q_out, q, key, value, k_codes, v_codes, (kv_scales,), cos_sin, positions,
+                              slot_mapping, interleaved)
     _check((_lib or load()).pa_rope_and_cache_q8(*args, _KV8_TYPES[k_codes.dtype],
-                                                 _raw_stream(stream)), "pa_rope_and_cache_q8")
+                                                 _raw_stream(stream, device)), "pa_rope_and_cache_q8")
 
 
 def pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim) -> int:
@@ -568,28 +568,31 @@ def new_window_workspace(num_seqs, num_heads, num_kv_heads, head_dim, device=Non
     return ws
 
 
-def _context_args(out, q, k_cache, v_cache, scales, block_tables, context_lens, max_context_len):
+def _context_args(device, out, q, k_cache, v_cache, scales, block_tables, context_lens,
+                  max_context_len):
     """Checks and leading arguments that the window attentions share."""
     assert q.dtype in _DTYPES and out.dtype == q.dtype and out.shape == q.shape
-    assert v_cache.shape == k_cache.shape and k_cache.shape[3] == q.shape[2]
-    assert v_cache.dtype == k_cache.dtype
+    assert v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
     assert block_tables.dtype == context_lens.dtype == torch.int32
     rows, width = block_tables.shape
     assert rows == context_lens.numel()
-    *caches, tables, lens = _pointers(torch.cuda.current_device(), out, q, k_cache, v_cache, *scales,
-                                      block_tables, context_lens)
+    *caches, tables, lens = _pointers(device, out, q, k_cache, v_cache, *scales, block_tables,
+                                      context_lens)
     return [*caches, tables, width, lens, int(max_context_len)]
 
 
-def _decode_args(out, q, k_cache, v_cache, scales, kinds, block_tables, context_lens,
-                 max_context_len, window, num_sinks, scale, workspace, stream):
+def _decode_args(out, q, k_cache, v_cache, scales, block_tables, context_lens, max_context_len,
+                 window, num_sinks, scale, workspace, stream):
     b, h, d = q.shape
-    nb, kvh, bs, _ = k_cache.shape
-    assert context_lens.numel() == b
-    return (*_context_args(out, q, k_cache, v_cache, scales, block_tables, context_lens,
-                           max_context_len), int(window), int(num_sinks), b, h, kvh, d, bs, nb, *kinds,
-            float(scale), *_pointers(torch.cuda.current_device(), workspace),
-            workspace.numel() * workspace.element_size(), _raw_stream(stream))
+    nb, kvh, bs, dk = k_cache.shape
+    device = torch.cuda.current_device()
+    assert context_lens.numel() == b and dk == d
+    args = _context_args(device, out, q, k_cache, v_cache, scales, block_tables, context_lens,
+                         max_context_len)
+    kinds = (_DTYPES[q.dtype], _KV8_TYPES[k_cache.dtype]) if scales else (_DTYPES[q.dtype],)
+    return (*args, int(window), int(num_sinks), b, h, kvh, d, bs, nb, *kinds, float(scale),
+            *_pointers(device, workspace), workspace.numel() * workspace.element_size(),
+            _raw_stream(stream, device))
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, window,
@@ -598,8 +601,8 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, max_c
     positions and the first `num_sinks`; grouped heads (q [B, H, D], cache
     [blocks, KVH, block_size, D])."""
     assert k_cache.dtype == q.dtype
-    args = _decode_args(out, q, k_cache, v_cache, (), (_DTYPES[q.dtype],), block_tables, context_lens,
-                        max_context_len, window, num_sinks, scale, workspace, stream)
+    args = _decode_args(out, q, k_cache, v_cache, (), block_tables, context_lens, max_context_len,
+                        window, num_sinks, scale, workspace, stream)
     _check((_lib or load()).pa_decode_window(*args), "pa_decode_window")
 
 
@@ -607,8 +610,7 @@ def pa_decode_q8(out, q, k_codes, v_codes, kv_scales, block_tables, context_lens
                  window, num_sinks, scale, workspace, stream=None):
     """pa_decode_window over the 8-bit cache with one scale per block and head."""
     _check_scales(kv_scales, k_codes, v_codes)
-    args = _decode_args(out, q, k_codes, v_codes, (kv_scales,),
-                        (_DTYPES[q.dtype], _KV8_TYPES[k_codes.dtype]), block_tables, context_lens,
+    args = _decode_args(out, q, k_codes, v_codes, (kv_scales,), block_tables, context_lens,
                         max_context_len, window, num_sinks, scale, workspace, stream)
     _check((_lib or load()).pa_decode_q8(*args), "pa_decode_q8")
 
@@ -618,15 +620,17 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, max_
     """pa_prefill with grouped heads, fp16 or bf16, and the visibility rule of
     pa_decode_window at each query's position."""
     t, h, d = q.shape
-    nb, kvh, bs, _ = k_cache.shape
+    nb, kvh, bs, dk = k_cache.shape
     b = context_lens.numel()
-    assert k_cache.dtype == q.dtype
+    device = torch.cuda.current_device()
+    assert k_cache.dtype == q.dtype and dk == d
     assert query_start_loc.dtype == torch.int32 and query_start_loc.numel() == b + 1
-    args = _context_args(out, q, k_cache, v_cache, (), block_tables, context_lens, max_context_len)
+    args = _context_args(device, out, q, k_cache, v_cache, (), block_tables, context_lens,
+                         max_context_len)
     _check((_lib or load()).pa_prefill_window(
-        *args, *_pointers(torch.cuda.current_device(), query_start_loc), t, int(max_query_len),
-        int(window), int(num_sinks), b, h, kvh, d, bs, nb, _DTYPES[q.dtype], float(scale),
-        _raw_stream(stream)), "pa_prefill_window")
+        *args, *_pointers(device, query_start_loc), t, int(max_query_len), int(window),
+        int(num_sinks), b, h, kvh, d, bs, nb, _DTYPES[q.dtype], float(scale),
+        _raw_stream(stream, device)), "pa_prefill_window")
 
 
 def pa_get_last_device_error() -> int:
