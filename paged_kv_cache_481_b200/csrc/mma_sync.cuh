@@ -102,19 +102,6 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
     return d;
 }
 
-__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b)
-{
-    return fma_f32x2(b, pack_f32x2(-1.0f, -1.0f), a);
-}
-
-// Maximum that is NaN where an argument is.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
 {
     uint64_t d;

@@ -85,7 +85,6 @@ constexpr int kThreads = (kMmaWarp + kTiles) * 32;
 constexpr uint32_t kTmemCols = 512, kTmemO = 2 * kN;
 constexpr float kRescaleLog2 = 8.0f;  // move the reference only past this growth
 constexpr float kShift = 7.0f;        // weights are 2^7 times the softmax's
-constexpr int kPolyEvery = 8;         // pairs of weights, of which one is a polynomial
 constexpr float kFloor = -1e30f;      // reference of a row that has seen nothing yet
 
 template <int D>
@@ -516,30 +515,9 @@ __device__ __forceinline__ float row_max(const uint32_t (&r)[kHalf])
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// 2^x of a pair by additions and multiplications: x = n + f with n whole and
-// |f| <= 1/2, a polynomial for 2^f (minimax of the relative error, 2.7e-6) and
-// n added to its exponent.  x below -126 counts as -126.
-__device__ __forceinline__ uint64_t exp2_poly_f32x2(uint64_t x)
-{
-    const float2 v = unpack_f32x2(x);
-    x = pack_f32x2(max_nan(v.x, -126.0f), max_nan(v.y, -126.0f));
-    const uint64_t whole = pack_f32x2(12582912.0f, 12582912.0f);  // 1.5 * 2^23: sums are whole
-    const uint64_t t = add_f32x2(x, whole);
-    const uint64_t f = sub_f32x2(x, sub_f32x2(t, whole));
-    uint64_t y = pack_f32x2(0.009570102207362652f, 0.009570102207362652f);
-    y = fma_f32x2(y, f, pack_f32x2(0.05591786280274391f, 0.05591786280274391f));
-    y = fma_f32x2(y, f, pack_f32x2(0.240247443318367f, 0.240247443318367f));
-    y = fma_f32x2(y, f, pack_f32x2(0.6931217908859253f, 0.6931217908859253f));
-    y = fma_f32x2(y, f, pack_f32x2(0.9999992847442627f, 0.9999992847442627f));
-    const uint32_t lo = uint32_t(y) + (uint32_t(t) << 23), hi = uint32_t(y >> 32) + (uint32_t(t >> 32) << 23);
-    return uint64_t(lo) | uint64_t(hi) << 32;
-}
-
 // P = 2^(c * s - m) of the row as 16-bit pairs over the first 32 columns of its
 // buffer; also the row sum of the unrounded P and the row maximum of s, which
-// nothing here waits for.  One pair in kPolyEvery goes through the polynomial,
-// which takes that share off the special-function unit (4 lanes a clock and
-// quarter of an SM).
+// nothing here waits for.
 template <bool kBf16>
 __device__ __forceinline__ void write_weights(uint32_t tS, const uint32_t (&r)[kHalf], float c, float m,
                                               float &sum, float &largest)
@@ -553,16 +531,11 @@ __device__ __forceinline__ void write_weights(uint32_t tS, const uint32_t (&r)[k
 #pragma unroll
         for (int i = 0; i < kHalf / 4; ++i) {
             const int e = part * (kHalf / 4) + i;
-            uint64_t x = fma_f32x2(uint64_t(r[2 * e]) | uint64_t(r[2 * e + 1]) << 32, cc, mm);
-            if (kPolyEvery > 0 && e % kPolyEvery == kPolyEvery - 1) {
-                x = exp2_poly_f32x2(x);
-            } else {
-                const float2 v = unpack_f32x2(x);
-                x = pack_f32x2(exp2_sfu(v.x), exp2_sfu(v.y));
-            }
-            total[e & 1] = add_f32x2(total[e & 1], x);
+            const uint64_t x = fma_f32x2(uint64_t(r[2 * e]) | uint64_t(r[2 * e + 1]) << 32, cc, mm);
             const float2 v = unpack_f32x2(x);
-            pk[i] = Half16<kBf16>::pack(v.x, v.y);
+            const float p0 = exp2_sfu(v.x), p1 = exp2_sfu(v.y);
+            total[e & 1] = add_f32x2(total[e & 1], pack_f32x2(p0, p1));
+            pk[i] = Half16<kBf16>::pack(p0, p1);
             top[e & 1] = max3f(top[e & 1], __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
         tmem_store16(tS + uint32_t(part * (kHalf / 4)), pk);

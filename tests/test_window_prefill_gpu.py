@@ -182,3 +182,27 @@ def test_whole_context_agrees_with_pa_prefill():
     ref, mass = attend64(q[300:], *paged.context64(1), list(range(130)), 700, 0, 0.1)
     bound = attention_bound(ref, mass, F16, F16) + 130 * 2.0 ** -24 * 8
     assert bool(((old[300:].double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("window,sinks", [(40, 0), (70, 5)])
+def test_hidden_rows_of_the_largest_magnitude_have_no_effect(dtype, window, sinks):
+    """Each position is hidden from some query of the same tile that its
+    neighbours see; with V = +-max there, any weight but zero would show."""
+    length, n, big = 300, 200, torch.finfo(dtype).max
+    paged = Paged([length], 1, 64, 16, dtype, seed=17)
+    q = paged.randn((n, 2, 64))
+    pos = torch.arange(length - n, length)
+    for at in (length - 1, 101, 110, 150, 175):   # seen by queries at .. at + window - 1 only
+        block, row = int(paged.tables[0, at // 16]), at % 16
+        keep = paged.k[block, 0, row].clone(), paged.v[block, 0, row].clone()
+        paged.k[block, 0, row], paged.v[block, 0, row] = 0, big
+        out = _prefill(paged, q, [n], window, sinks, 0.125)
+        hidden = ~((at <= pos) & ((at > pos - window) | (at < sinks)))
+        k, v = paged.context64(0)
+        v = v.clone()
+        v[at] = 0                              # whatever it is, where it is hidden
+        ref, mass = attend64(q, k, v, pos.tolist(), window, sinks, 0.125)
+        bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
+        assert bool(((out.double() - ref).abs() <= bound)[hidden.cuda()].all())
+        paged.k[block, 0, row], paged.v[block, 0, row] = keep
