@@ -644,6 +644,10 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             issue(stage ^ 1);
             if (!dead && !mbar_wait_bounded(smem_u32(&s_full[warp][stage]), phase)) {
                 atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                // once more for the copies in flight, which must not land
+                // after the block has ended
+                mbar_wait_bounded(smem_u32(&s_full[warp][stage]), phase);
+                mbar_wait_bounded(smem_u32(&s_full[warp][stage ^ 1]), phase ^ uint32_t(stage));
                 dead = true;
             }
             dead = __any_sync(kFullMask, dead);
