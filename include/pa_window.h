@@ -149,7 +149,9 @@ PA_API pa_status pa_decode_window(void *out, const void *q, const void *k_cache,
 
 /*
  * pa_decode_window over the 8-bit cache: K_t = s_k * code, V_t = s_v * code
- * with the scales of the block and head that hold t; q and out in `dtype`.
+ * with the scales of the block and head that hold t; q and out in `dtype`.  The
+ * weights enter the product with V times s_v, in fp16 relative to the largest:
+ * what is below 2^-31 of it is lost.
  * About half the bytes of pa_decode_window.
  */
 PA_API pa_status pa_decode_q8(void *out, const void *q, const void *k_codes, const void *v_codes,

@@ -11,6 +11,13 @@
 // A thread works on a "unit" of 16 elements of a row, two 16-byte pieces that
 // hold whole pairs: elements [8u, 8u + 8) and [r/2 + 8u, ...) of a
 // half-split rotation of r dims, else 16 neighbouring elements.
+//
+// Measured (kernel alone, one B200): 9 packed prompts, H 32, KVH 8, bf16:
+// 43.6 us, 5.6 TB/s, 86 % of a plain copy's rate (the rest is the first and
+// the last wave); 32 tokens of 40 heads: 4.2 us, a launch and three dependent
+// loads.  The 8-bit write: 12 chunks, H 32, KVH 8, e4m3: 39 us, 3.6 TB/s, bound
+// by the chain slot -> rows -> angles -> maximum -> codes with 64 registers a
+// thread; 256 single tokens of 40 heads: 8.3 us.
 #pragma once
 
 #include <cstdint>
@@ -388,7 +395,9 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
 // query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A token alone in
 // its run (a decode step) has its heads done side by side, D / 16 lanes each
 // for K and for V.  The heads of a longer run are shared out over the CTAs of
-// its first kSpan tokens, a CTA a head (64 threads K, 64 threads V).
+// its first kSpan tokens, a CTA a head (64 threads K, 64 threads V).  The q
+// rows are rotated by the same CTAs: with CTAs of their own the streaming part
+// waited behind the dependent one (55 us against 39 on 12 chunks).
 template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(const RopeParams p)
 {

@@ -25,18 +25,20 @@ struct WindowWorkspace {
     size_t ml_off, ticket_off, total;
 };
 
-// query heads of a unit: 8, or 16 for larger groups
-int unit_heads(int group)
+// Query heads of a unit: 8, or 16 for larger groups when that leaves units
+// enough (both sides measured in window_decode_kernel.cuh).
+int unit_heads(int num_seqs, int num_kv_heads, int group)
 {
-    return group <= 8 ? 8 : 16;
+    constexpr int64_t kFewUnits = 32;
+    return group <= 8 || int64_t(num_seqs) * num_kv_heads * ((group + 15) / 16) <= kFewUnits ? 8 : 16;
 }
 
 WindowWorkspace window_workspace(int num_seqs, int num_heads, int num_kv_heads)
 {
     WindowWorkspace w{};
-    const int group = num_heads / num_kv_heads, per = unit_heads(group);
+    const int group = num_heads / num_kv_heads;
     const size_t slots = size_t(pa::kWdSlots);
-    const size_t units = size_t(num_seqs) * num_kv_heads * ((group + per - 1) / per);
+    const size_t units = size_t(num_seqs) * num_kv_heads * ((group + 7) / 8);
     w.ml_off = align256(slots * 16 * 128 * sizeof(float));
     w.ticket_off = w.ml_off + align256(slots * 16 * sizeof(float2));
     w.total = w.ticket_off + align256((units > 0 ? units : 1) * sizeof(unsigned));
@@ -133,7 +135,7 @@ pa_status window_decode(void *out, const void *q, const void *k, const void *v,
     p.heads = num_heads;
     p.kv_heads = num_kv_heads;
     p.group = num_heads / num_kv_heads;
-    const int per = unit_heads(p.group);
+    const int per = unit_heads(num_seqs, num_kv_heads, p.group);
     p.row_tiles = (p.group + per - 1) / per;
     p.log2_bs = __builtin_ctz(unsigned(block_size));
     p.num_blocks = num_blocks;

@@ -16,22 +16,44 @@
 // products, sums and accumulators of the other order, and K and V are read
 // once per group.  (tcgen05 needs 64 rows and more and its operands through
 // one more hop; at these sizes the copies would wait for it.)
+// Measured (kernel alone, one B200): 32 sequences of 256 to 2048, window 1024,
+// 40 heads, fp16: 94 us, 6.1 TB/s; 256 of 1000 to 32768, window 4096, 8 K/V
+// heads, bf16: 620 us, 6.7 TB/s; 128 of 1024 to 16384, 8 K/V heads, e4m3:
+// 370 to 400 us, 5.8 to 6.2 TB/s, where the conversions of codes take the ALU
+// 60 % of the time.  Small calls are bound by latency: lengths, table, tiles,
+// then the join, 14.5 us for one sequence and a window of 4100.
 //
 // Layout of the work: a "unit" is (sequence, K/V head, 8 * kNq query heads);
 // its visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens
 // at D = 128 in 16 bits).  The kernel's blocks count the tiles and choose, all
 // alike, one of three ways to share them out:
-//   * much work: the tiles of all units, unit after unit, are cut into equal
+//   * as many units as CTAs or fewer: each unit is cut into even parts of at
+//     least 16 tiles, one a CTA, whose four warps take its tiles in turn and
+//     merge in shared memory;
+//   * as many units as warps or fewer: the same with parts for single warps;
+//   * else the tiles of all units, unit after unit, are cut into equal
 //     contiguous ranges, one a warp, which needs nobody else until the end of
 //     a unit that straddles ranges.  Cuts within 2 tiles of a unit's end move
 //     there.
-//   * few units: each unit is cut into even parts of at least 16 tiles, one a
-//     CTA, whose four warps take its tiles in turn and merge in shared memory.
-//   * little work in many units: the same with parts for single warps.
-// (A second segment or a straddling unit costs a warp 4 us or more, as much as
-// 8 tiles; so little work is better uneven than cut.)  A cut unit's parts go
-// to the workspace and the last one to arrive merges them in order, so the
-// result does not depend on the order of arrival.
+// A cut unit's parts go to the workspace and the last one to arrive merges
+// them in order, so the result does not depend on the order of arrival.
+// Ranges also take over from parts when there is much work (16 tiles a warp)
+// of unlike lengths: when parts of up to 1.75 (8 bits: 1.25) times a worker's
+// share do not give each worker one at most, or the longest is more than 1.3
+// times their mean.  Memory does not mind that a third of the warps have no
+// part, as long as the others end together, and a second segment or a
+// straddling unit costs a warp 4 us or more; the conversions of 8-bit codes
+// do mind.  Measured, parts against ranges (us, D = 128, 16 bits; units of 8
+// heads): 8 units of 4100 tokens 14.5 / 90; 128 of 4100 52 / 56 (single
+// warps 53); 256 of 4100 88 / 97; 1280 of 1028 109 / 112; 1280 of 256 to 1028
+// 94 / 102; but 384 of 512 to 4100 85 / 80, and 1024 of 1024 to 16384 in 8
+// bits 436 / 396.  8 units of 16 heads and 8000 tokens: CTAs 25, single warps
+// 57.
+//
+// kNq: groups of more than 8 heads take 16 columns at a time, which reads K
+// and V half as often (128 such units of 8000 tokens: 94 us against 119), but
+// 8 at a time when there are 32 such units or fewer, twice the parts to run
+// side by side (8 units of 8000: 20.6 us against 24.2, 32: 32.4 against 35).
 //
 // Each warp keeps a ring of kStages tiles full, across units: one lane per
 // block run issues TMA boxes (K and V) that complete an mbarrier, with the
@@ -47,7 +69,8 @@
 // exact in it): the query row is scaled by a power of two so that its largest
 // component is near 2^14, exact for every component above 2^-28 of it; a
 // block's s_v is folded into its weights relative to a running power of two
-// at or above the largest s_v so far.
+// at or above the largest s_v so far (a block's values count down to 2^-31 of
+// the largest s_v times the largest weight).
 #pragma once
 
 #include <cuda.h>
@@ -88,7 +111,10 @@ constexpr int kWdMaxRanges = kWdMaxCtas * kWdWarps;
 constexpr float kWdShift = 7.0f;     // weights are 2^7 times the softmax's
 constexpr float kWdRescale = 8.0f;   // move the reference only past this growth
 constexpr int kWdSnap = 2;           // cuts of ranges this close to a unit's end move there
-constexpr int kWdMuchWork = 16;      // tiles a warp from which on ranges are used
+constexpr int kWdMuchWork = 16;      // tiles a warp below which ranges are not worth it
+constexpr int kWdCuts = 2;           // lengths of parts that are tried
+constexpr int kWdCuts8 = 1;          // of them, those that a large 8-bit batch may use
+constexpr float kWdAlike = 1.3f;     // longest part of a large batch, times their mean
 // least tiles of a part: one for a CTA (4 a warp), one for a warp
 constexpr int kWdTeamTiles = 16, kWdWarpTiles = 8;
 constexpr int kWdSlots = 2 * kWdMaxRanges;  // partial results: 2 a range, or 1 a part
@@ -339,8 +365,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     constexpr bool kEight = W::kEight, kE4m3 = kStore == KvStore::kE4m3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_full[kWdWarps][kStages];
-    __shared__ long long s_scan[kWdWarps], s_parts[kWdWarps], s_before[kWdThreads];
-    __shared__ int s_live[kWdWarps], s_last;
+    __shared__ long long s_scan[kWdWarps], s_before[kWdThreads];
+    __shared__ int s_live[kWdWarps], s_parts[kWdWarps][kWdCuts], s_last;
     __shared__ WindowPlan plan;
     // of each warp, the segment it works on and the one it fetches; what every
     // tile needs of them is kept in registers
@@ -400,37 +426,64 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     if (total == 0)
         return;
     const long long ctas = gridDim.x, warps = ctas * kWdWarps;
-    const bool little = total < kWdMuchWork * warps;
-    const bool team = all_units <= ctas / 4 || (little && all_units <= ctas);
-    const bool ranges = !team && !(little && all_units <= warps);
+    const bool few = all_units <= ctas / 4, little = total < kWdMuchWork * warps;
+    const bool for_ctas = all_units <= ctas;
+    bool ranges = all_units > warps;
     long long items = 0;
     int chunk = 0;
-    if (!ranges) {                 // the same scan for parts, at most 1.5 a worker
-        const long long even = team ? ceil_div(total, max(ctas - all_units, ctas / 2))
-                                    : ceil_div(2 * total, warps);
-        chunk = max(team ? kWdTeamTiles : kWdWarpTiles, int(min(even, (long long)INT_MAX / 2)));
-        mine = 0;
+    if (!ranges) {                 // how long the longest part must be for one part a worker
+        const long long workers = for_ctas ? ctas : warps;
+        int longest[kWdCuts], sum[kWdCuts] = {};
+#pragma unroll
+        for (int j = 0; j < kWdCuts; ++j) {
+            constexpr float kTimes[kWdCuts] = {1.25f, 1.75f};
+            const float even = few ? float(total) / float(ctas - all_units)  // (always long enough)
+                                   : kTimes[j] * float(total) / float(workers);
+            longest[j] = max(for_ctas ? kWdTeamTiles : kWdWarpTiles, int(fminf(even, 1e9f)) + 1);
+        }
         for (int b = sb0; b < sb1; ++b) {
             WindowView v{};
             v.set<kTile>(p.lens[b], p.max_len, p.window, p.sinks);
-            mine += (long long)WindowSegment::cut(v.tiles, chunk) * units;
-        }
-        incl = mine;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long o = __shfl_up_sync(kFullMask, incl, off);
-            incl += lane >= off ? o : 0;
+            for (int j = 0; j < kWdCuts; ++j)
+                sum[j] += WindowSegment::cut(v.tiles, longest[j]) * units;
         }
-        if (lane == 31)
-            s_parts[warp] = incl;
+        int own[kWdCuts];
+#pragma unroll
+        for (int j = 0; j < kWdCuts; ++j) {
+            own[j] = sum[j];
+            sum[j] = __reduce_add_sync(kFullMask, sum[j]);
+            if (lane == 0)
+                s_parts[warp][j] = sum[j];
+        }
         __syncthreads();
-        excl = incl - mine;
+        int pick = 0, parts = 0;
+        bool fits = false;
 #pragma unroll
-        for (int w = 0; w < kWdWarps; ++w) {
-            excl += w < warp ? s_parts[w] : 0;
-            items += s_parts[w];
+        for (int j = kWdCuts - 1; j >= 0; --j) {
+            int all = 0;
+#pragma unroll
+            for (int w = 0; w < kWdWarps; ++w)
+                all += s_parts[w][j];
+            if (j == kWdCuts - 1 || all <= workers)
+                pick = j, parts = own[j], chunk = longest[j], items = all, fits = all <= workers;
+        }
+        const bool alike = float(chunk) * float(items) <= kWdAlike * float(total);
+        ranges = !(few || little || (fits && alike && (!kEight || pick < kWdCuts8)));
+        if (!ranges) {             // the same scan for the parts
+            int upto = parts;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(kFullMask, upto, off);
+                upto += lane >= off ? o : 0;
+            }
+            excl = upto - parts;
+#pragma unroll
+            for (int w = 0; w < kWdWarps; ++w)
+                excl += w < warp ? s_parts[w][pick] : 0;
         }
     }
+    const bool team = for_ctas && !ranges;
     s_before[tid] = excl;
     if (tid == 0)
         plan = WindowPlan{items, total, team ? ctas : warps, s_before, ranges, chunk, units, per};

@@ -12,6 +12,11 @@
 // and one exponential a pair on the special-function unit (16 a clock and
 // SM: as long as the matrix work at D = 128, twice as long at D = 64); for a
 // few queries a sequence, the read of K and V.
+// Measured (kernel alone, one B200): one prompt of 8192, window 4096, H 32,
+// KVH 8, bf16: 376 us, 1.10 PFLOP/s of visible pairs, two thirds of the library
+// product's rate; 8 chunks of 100 to 512 queries, 40 heads, fp16: 102 us, 4 to
+// 5 us of it between items; 16 sequences of 1 to 7 queries: 23 us, one wave of
+// dependent steps of 0.9 us.
 //
 // Layout of the work: the 128 rows of a query tile are tq = floor(128 / G)
 // tokens times the G query heads of one K/V head, so K and V are read once

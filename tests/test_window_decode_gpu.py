@@ -50,6 +50,26 @@ def test_long_contexts_are_split_and_merged(dtype, codes):
         assert torch.equal(decode(paged, q, 30000, 0, 0.09, workspace=ws), first)
 
 
+@pytest.mark.parametrize("dtype,codes", STORES[1:3])
+@pytest.mark.parametrize("lens,heads,kvh", [
+    ([4100] * 16, 32, 8),                              # a unit to a few CTAs
+    ([2100] * 47 + [0], 16, 8),                        # a unit a CTA
+    ([1028] * 30 + [700, 1], 40, 40),                  # a unit a warp
+    ([500 + 75 * i for i in range(48)], 32, 8),        # unlike lengths: equal ranges
+    ([1100] * 60 + [3, 0, 999], 32, 32),               # more units than warps
+    ([3000, 2999, 17], 64, 4), ([2000] * 20, 64, 4),   # 16 heads a group, few and many
+    ([900] * 7, 40, 2),                                # 20 heads a group
+])
+def test_large_batches_are_shared_out(dtype, codes, lens, heads, kvh):
+    paged = Paged(lens, kvh, 128, 16, dtype, seed=heads + kvh, codes=codes)
+    q = paged.randn((len(lens), heads, 128))
+    ws = binding.new_window_workspace(len(lens), heads, kvh, 128)
+    out = decode(paged, q, 5000, 0, 0.09, workspace=ws)
+    assert binding.pa_get_last_device_error() == 0
+    check_decode(paged, q, out, 5000, 0, 0.09)
+    assert torch.equal(decode(paged, q, 5000, 0, 0.09, workspace=ws), out)
+
+
 @pytest.mark.parametrize("dtype,codes", STORES[:4])
 def test_blocks_that_the_window_left_are_not_looked_at(dtype, codes):
     """Table entries of blocks without a visible position may be anything, and
