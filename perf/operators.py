@@ -23,52 +23,52 @@ def listed():
     return [
         # one decode step of 32 sequences with 40 heads of 128 (13B shapes):
         # the smallest call, all latency
-        dict(name="rope cache decode step", op="rope_cache", dtype="f16", heads=40, kv_heads=40,
+        dict(name="rope cache, decode step", op="rope_cache", dtype="f16", heads=40, kv_heads=40,
              head_dim=128, block_size=16, seqs=32, new_min=1, new_max=1, start_max=2048,
              rotary=128, interleaved=False, padding=0),
         # prompts and chunks of a packed batch with grouped heads and padded rows at its end
-        dict(name="rope cache packed prompts", op="rope_cache", dtype="bf16", heads=32, kv_heads=8,
+        dict(name="rope cache, packed prompts", op="rope_cache", dtype="bf16", heads=32, kv_heads=8,
              head_dim=128, block_size=16, seqs=9, new_min=37, new_max=2048, start_max=8192,
              rotary=64, interleaved=True, padding=21),
         # a serving batch's decode step into the 8-bit cache: most blocks are
         # part full, so older rows of a block meet a larger scale
-        dict(name="rope cache q8 decode step", op="rope_cache_q8", dtype="f16", heads=40,
+        dict(name="rope cache q8, decode step", op="rope_cache_q8", dtype="f16", heads=40,
              kv_heads=40, head_dim=128, block_size=16, seqs=256, new_min=1, new_max=1,
              start_max=4096, rotary=128, interleaved=False, padding=0, codes="int8"),
         # chunks that start and end inside a block
-        dict(name="rope cache q8 chunks", op="rope_cache_q8", dtype="bf16", heads=32, kv_heads=8,
+        dict(name="rope cache q8, chunks", op="rope_cache_q8", dtype="bf16", heads=32, kv_heads=8,
              head_dim=128, block_size=32, seqs=12, new_min=100, new_max=900, start_max=8192,
              rotary=128, interleaved=False, padding=5, codes="e4m3"),
         # one long stream of one user: only the window's and the first blocks are still held
-        dict(name="window decode one stream", op="decode_window", dtype="bf16", heads=32,
+        dict(name="window decode, one stream", op="decode_window", dtype="bf16", heads=32,
              kv_heads=8, head_dim=128, block_size=16, seqs=1, len_min=131071, len_max=131071,
              window=4096, sinks=4),
         # the 13B decode batch with a 1024-token window
-        dict(name="window decode 13B batch", op="decode_window", dtype="f16", heads=40,
+        dict(name="window decode, 13B batch", op="decode_window", dtype="f16", heads=40,
              kv_heads=40, head_dim=128, block_size=16, seqs=32, len_min=256, len_max=2048,
              window=1024, sinks=4),
         # a large serving batch with grouped heads; many contexts pass the window
-        dict(name="window decode serving batch", op="decode_window", dtype="bf16", heads=64,
+        dict(name="window decode, serving batch", op="decode_window", dtype="bf16", heads=64,
              kv_heads=8, head_dim=128, block_size=16, seqs=256, len_min=1000, len_max=32768,
              window=4096, sinks=4),
         # a few draft tokens of each sequence to be verified
-        dict(name="window prefill drafts", op="prefill_window", dtype="bf16", heads=32, kv_heads=8,
+        dict(name="window prefill, drafts", op="prefill_window", dtype="bf16", heads=32, kv_heads=8,
              head_dim=128, block_size=16, seqs=16, new_min=1, new_max=7, len_min=300,
              len_max=4096, window=1024, sinks=4),
         # chunks of several prompts, each continuing its cached context
-        dict(name="window prefill chunks", op="prefill_window", dtype="f16", heads=40, kv_heads=40,
+        dict(name="window prefill, chunks", op="prefill_window", dtype="f16", heads=40, kv_heads=40,
              head_dim=128, block_size=16, seqs=8, new_min=100, new_max=512, len_min=600,
              len_max=2048, window=1000, sinks=0),
         # one whole long prompt
-        dict(name="window prefill long prompt", op="prefill_window", dtype="bf16", heads=32,
+        dict(name="window prefill, long prompt", op="prefill_window", dtype="bf16", heads=32,
              kv_heads=8, head_dim=128, block_size=16, seqs=1, new_min=8192, new_max=8192,
              len_min=8192, len_max=8192, window=4096, sinks=4),
         # a small batch over the 8-bit cache, whole contexts
-        dict(name="q8 decode small batch", op="decode_q8", dtype="f16", heads=40, kv_heads=40,
+        dict(name="q8 decode, small batch", op="decode_q8", dtype="f16", heads=40, kv_heads=40,
              head_dim=128, block_size=16, seqs=4, len_min=17, len_max=2047, window=2047, sinks=0,
              codes="int8"),
         # a large batch over the 8-bit cache, whole contexts, grouped heads
-        dict(name="q8 decode large batch", op="decode_q8", dtype="bf16", heads=64, kv_heads=8,
+        dict(name="q8 decode, large batch", op="decode_q8", dtype="bf16", heads=64, kv_heads=8,
              head_dim=128, block_size=32, seqs=128, len_min=1024, len_max=16384, window=16384,
              sinks=0, codes="e4m3"),
     ]
