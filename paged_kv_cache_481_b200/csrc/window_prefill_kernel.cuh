@@ -657,6 +657,9 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                         tmem_store16(tO + uint32_t(cc * 16), o);
                     }
+                    // stores to one place have no order of their own: the
+                    // weights written first must not land on the next ones
+                    tmem_wait_st();
                     l *= alpha;
                     m_ref = m_new;
                 }

@@ -206,3 +206,27 @@ def test_hidden_rows_of_the_largest_magnitude_have_no_effect(dtype, window, sink
         bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
         assert bool(((out.double() - ref).abs() <= bound)[hidden.cuda()].all())
         paged.k[block, 0, row], paged.v[block, 0, row] = keep
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,block_size", [(64, 8), (128, 32)])
+def test_scores_that_jump_far_past_the_reference(dtype, d, block_size):
+    """Single tokens score hundreds above all before them, first, last and in
+    the middle of a step: against the reference as it stood, their weights are
+    past the type's range, and those that count are written over them."""
+    length, n, group = 700, 300, 4
+    paged = Paged([length], 2, d, block_size, dtype, seed=23)
+    for t in range(length):
+        paged.k[int(paged.tables[0, t // block_size]), :, t % block_size] = 0
+    for i, t in enumerate((256, 383, 389, 448, 511, 540, 639, 640, 671, 690, 699)):
+        paged.k[int(paged.tables[0, t // block_size]), :, t % block_size, 0] = 200.0 * (i + 1)
+    q = torch.zeros((n, 2 * group, d), dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([1.0, 0.5, 0.25, 0.0], device="cuda").repeat(2).to(dtype)
+    out = _prefill(paged, q, [n], 600, 3, 1.0)
+    assert binding.pa_get_last_device_error() == 0
+    k, v = paged.context64(0)
+    ref, mass = attend64(q, k, v, list(range(length - n, length)), 600, 3, 1.0)
+    # scores are exact; tokens of one score share the rounding of c s - m, and
+    # those of a lower one are 50 and more below it, so their weights vanish
+    bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
+    assert bool(((out.double() - ref).abs() <= bound).all())
