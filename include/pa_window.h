@@ -170,9 +170,10 @@ PA_API pa_status pa_decode_q8(void *out, const void *q, const void *k_codes, con
  * Runs on the tensor cores (tcgen05); scores and sums fp32, the weights enter
  * the product with V in the cache's 16-bit type.  scale must be finite and
  * > 0.  Rows of q and out that belong to no sequence are left as they are.
- * A V row that is not finite may reach queries of its sequence that are less
- * than 256 positions away even where the mask hides it from them; rows that
- * no such query sees have no effect.  n_b > L_b or > max_query_len,
+ * A V row that is not finite, and that some query of its sequence sees, may
+ * also reach queries less than 256 positions away from such a query, though
+ * the mask hides it from them (a weight of zero times infinity is NaN); rows
+ * that no query sees have no effect.  n_b > L_b or > max_query_len,
  * or rows outside q, are recorded (PA_DEVERR_CONTEXT_LEN) and that sequence
  * is skipped.
  */

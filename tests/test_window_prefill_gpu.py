@@ -230,3 +230,29 @@ def test_scores_that_jump_far_past_the_reference(dtype, d, block_size):
     # those of a lower one are 50 and more below it, so their weights vanish
     bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
     assert bool(((out.double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads,kvh", [(2, 2), (8, 2), (7, 1)])
+@pytest.mark.parametrize("window,sinks,at", [(300, 0, 700), (40, 5, 901), (900, 0, 600),
+                                             (90, 901, 900), (500, 3, 1023)])
+def test_how_far_a_row_that_is_not_finite_reaches(dtype, heads, kvh, window, sinks, at):
+    """V at position `at` is infinite.  Queries that see it get no finite
+    value; those 256 positions and more away from all of them get what they
+    would without it."""
+    length, n = 2000, 1700
+    paged = Paged([length], kvh, 64, 16, dtype, seed=37)
+    paged.v[int(paged.tables[0, at // 16]), :, at % 16] = float("inf")
+    q = paged.randn((n, heads, 64))
+    out = _prefill(paged, q, [n], window, sinks, 0.125)
+    pos = torch.arange(length - n, length)
+    sees = (at <= pos) & ((at > pos - window) | (at < sinks))
+    far = ((pos[:, None] - pos[sees][None]).abs() >= 256).all(1)
+    assert bool(sees.any()) and bool(far.any())
+    assert not bool(out[sees.cuda()].isfinite().any())
+    k, v = paged.context64(0)
+    v = v.clone()
+    v[at] = 0                                  # hidden from all queries looked at
+    ref, mass = attend64(q, k, v, pos.tolist(), window, sinks, 0.125)
+    bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
+    assert bool(((out.double() - ref).abs() <= bound)[far.cuda()].all())
