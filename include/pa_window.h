@@ -102,7 +102,9 @@ PA_API pa_status pa_rope_and_cache(void *q_out, int64_t q_out_stride, const void
  * Rows behind the new ones keep their codes (a later write replaces them).
  * A block whose rows are all zero has s = 0 and codes 0.  Rows holding inf or
  * NaN make their block's values unspecified.  A block is written by one run
- * of tokens per call.  Other arguments and rules as pa_rope_and_cache; a
+ * of tokens per call: one that the call's tokens come back to (interleaved
+ * sequences, a slot given twice) is recorded (PA_DEVERR_SLOT) and its values
+ * unspecified.  Other arguments and rules as pa_rope_and_cache; a
  * position outside the table is recorded and its row's values unspecified.
  */
 PA_API pa_status pa_rope_and_cache_q8(void *q_out, int64_t q_out_stride, const void *q,

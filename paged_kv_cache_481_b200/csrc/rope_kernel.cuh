@@ -41,6 +41,7 @@ struct RopeParams {
     int block_size, num_blocks;
     int scale_heads;                // heads of a block's scale row (kv heads rounded up to even)
     int groups;                     // 8-bit kernel: CTAs per token
+    int checkers;                   // 8-bit kernel: CTAs that look for blocks with two runs
     unsigned int *err;
 };
 
@@ -391,7 +392,36 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
         *my_scale = scale.scale;
 }
 
-// Grid: p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
+// Records blocks of [first, first + kCheckBlocks) that the call's tokens enter
+// more than once: a block's rows, older ones and scale are one run's to write.
+// A bit a block, set by the first token of each run (unless its position is
+// outside the table, which is recorded by itself).
+constexpr int kCheckBlocks = 32768;
+
+__device__ __forceinline__ void check_runs(const RopeParams &p, int64_t first, uint32_t (&seen)[kCheckBlocks / 32])
+{
+    const int log2_bs = __ffs(p.block_size) - 1;
+    const int64_t blocks = min(int64_t(kCheckBlocks), p.num_blocks - first);
+    for (int i = threadIdx.x; i < (blocks + 31) / 32; i += kRopeThreads)
+        seen[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.num_tokens; i += kRopeThreads) {
+        const int64_t slot = p.slots[i], before = i > 0 ? p.slots[i - 1] : -1;
+        const int64_t at = (slot >> log2_bs) - first;
+        if (slot < 0 || at < 0 || at >= blocks || (before == slot - 1 && (slot & (p.block_size - 1)) != 0))
+            continue;
+        const int64_t pos = p.rotary > 0 ? p.positions[i] : 0;
+        if (pos < 0 || (p.rotary > 0 && pos >= p.max_position))
+            continue;
+        const uint32_t bit = 1u << (at & 31);
+        if (atomicOr(&seen[at >> 5], bit) & bit)
+            atomicOr(p.err, PA_DEVERR_SLOT);
+    }
+}
+
+// Grid: p.checkers CTAs, which look for blocks that two runs write (5 us next
+// to the others' 8 and more), then p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
 // query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A token alone in
 // its run (a decode step) has its heads done side by side, D / 16 lanes each
 // for K and for V.  The heads of a longer run are shared out over the CTAs of
@@ -402,11 +432,17 @@ template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(const RopeParams p)
 {
     __shared__ float both[2][2];
+    __shared__ uint32_t seen[kCheckBlocks / 32];
     grid_dependency_wait();
     allow_dependent_launch();
+    if (int(blockIdx.x) < p.checkers) {
+        check_runs(p, int64_t(blockIdx.x) * kCheckBlocks, seen);
+        return;
+    }
+    const int cta = int(blockIdx.x) - p.checkers;
     constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kSpan = 2 * kHeads;
     constexpr int kPasses = 2, kRows = kRopeThreads / kUnits * kPasses;
-    const int i = int(blockIdx.x) / p.groups, g = int(blockIdx.x) % p.groups;
+    const int i = cta / p.groups, g = cta % p.groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     // slots of the kSpan tokens before this one and of those from it on
     const int j = i - kSpan + lane;

@@ -304,3 +304,39 @@ def test_tensors_of_another_device_or_layout_are_refused():
     with pytest.raises(binding.PAError):  # a token stride that is not a multiple of 8
         odd = torch.zeros((2, 68), dtype=F16, device="cuda")[:, :64].unsqueeze(1)
         call(odd, odd, x, x, kc, vc)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_blocks_that_a_call_comes_back_to_are_recorded(kind):
+    """The 8-bit write takes a block's tokens side by side: interleaved
+    sequences and slots given twice set the error bit, wherever in the pool
+    they are; runs in any order, split by padding between blocks, do not."""
+    kvh, d, bs, nb = 1, 64, 8, 70001
+    kc, vc = (torch.zeros((nb, kvh, bs, d), device="cuda").to(CODES[kind][0]) for _ in "kv")
+    scales = torch.zeros((nb, 2, 2), device="cuda")
+    binding.pa_get_last_device_error()
+
+    def recorded(slots):
+        x = torch.ones((len(slots), kvh, d), dtype=F16, device="cuda")
+        binding.pa_rope_and_cache_q8(torch.empty_like(x), x, x, x, kc, vc, scales, None, None,
+                                     torch.tensor(slots, device="cuda"))
+        return binding.pa_get_last_device_error()
+
+    for base in (0, 3, 32767, 32768, 65535, 65536, nb - 3):
+        a, b = base * bs, (base + 2) * bs
+        assert recorded([a, a + 1, a + 2, b, b + 1]) == 0
+        assert recorded([a, b, a + 1, b + 1]) == binding.PA_DEVERR_SLOT    # drafts of two sequences
+        assert recorded([b, a, a]) == binding.PA_DEVERR_SLOT               # a slot twice
+        assert recorded([a, -1, a + 1]) == binding.PA_DEVERR_SLOT          # padding inside a run
+        assert recorded([a + 1, a]) == binding.PA_DEVERR_SLOT              # not in order
+        assert recorded([a + 6, a + 7, b, -1, a + 8, a + 9, -1]) == 0      # the next block, padding
+    order = torch.randperm(nb, generator=torch.Generator().manual_seed(1))[:3000].tolist()
+    runs = [list(range(b * bs + i % 8, b * bs + i % 8 + 1 + i % (8 - i % 8))) for i, b in enumerate(order)]
+    assert recorded(sum(runs, [])) == 0
+    runs.append([order[7] * bs + 7])            # far from the first run of its block
+    assert recorded(sum(runs, [])) == binding.PA_DEVERR_SLOT
+    # what was not touched twice holds its values
+    codes, scale = kc[order[8:]].float(), scales[order[8:], 0, 0]
+    first = torch.tensor([r[0] % bs for r in runs[8:-1]], device="cuda")
+    got = codes[torch.arange(len(first), device="cuda"), 0, first, 0] * scale
+    assert bool(((got - 1).abs() < 2.0 ** -20).all())
