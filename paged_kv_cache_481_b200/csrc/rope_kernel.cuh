@@ -41,7 +41,7 @@ struct RopeParams {
     int block_size, num_blocks;
     int scale_heads;                // heads of a block's scale row (kv heads rounded up to even)
     int groups;                     // 8-bit kernel: CTAs per token
-    int checkers;                   // 8-bit kernel: CTAs that look for blocks with two runs
+    int checkers, check_blocks;     // 8-bit kernel: CTAs that look for blocks with two runs, blocks of each
     unsigned int *err;
 };
 
@@ -392,36 +392,51 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
         *my_scale = scale.scale;
 }
 
-// Records blocks of [first, first + kCheckBlocks) that the call's tokens enter
-// more than once: a block's rows, older ones and scale are one run's to write.
-// A bit a block, set by the first token of each run (unless its position is
-// outside the table, which is recorded by itself).
-constexpr int kCheckBlocks = 32768;
+// Records blocks from `first` on, p.check_blocks of them, that the call's tokens
+// enter more than once: a block's rows, older ones and scale are one run's to
+// write.  A bit a block, set by the first token of each run.  (A second one
+// whose position is outside the table is recorded for that.)
+// The bit map takes 512 bytes (4096 blocks a CTA) for pools up to 64 such
+// parts, else 4 KB: next to 4 KB a CTA the L1 holds fewer of the rows that long
+// runs read twice (20 runs of 100 to 300 tokens, one K/V head: 25.6 us, with
+// 512 bytes or none 24.5), but every one of these CTAs passes over all slots,
+// and hundreds of them would be in the others' way.
+constexpr int kCheckFew = 4096, kCheckMany = 32768, kCheckParts = 64;
 
-__device__ __forceinline__ void check_runs(const RopeParams &p, int64_t first, uint32_t (&seen)[kCheckBlocks / 32])
+__device__ __forceinline__ void check_runs(const RopeParams &p, int64_t first, uint32_t *seen)
 {
     const int log2_bs = __ffs(p.block_size) - 1;
-    const int64_t blocks = min(int64_t(kCheckBlocks), p.num_blocks - first);
+    const int64_t blocks = min(int64_t(p.check_blocks), p.num_blocks - first);
     for (int i = threadIdx.x; i < (blocks + 31) / 32; i += kRopeThreads)
         seen[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = threadIdx.x; i < p.num_tokens; i += kRopeThreads) {
-        const int64_t slot = p.slots[i], before = i > 0 ? p.slots[i - 1] : -1;
-        const int64_t at = (slot >> log2_bs) - first;
-        if (slot < 0 || at < 0 || at >= blocks || (before == slot - 1 && (slot & (p.block_size - 1)) != 0))
-            continue;
-        const int64_t pos = p.rotary > 0 ? p.positions[i] : 0;
-        if (pos < 0 || (p.rotary > 0 && pos >= p.max_position))
-            continue;
-        const uint32_t bit = 1u << (at & 31);
-        if (atomicOr(&seen[at >> 5], bit) & bit)
-            atomicOr(p.err, PA_DEVERR_SLOT);
+    constexpr int kAhead = 4;      // loads in flight: one CTA passes over all the call's slots
+    for (int i0 = threadIdx.x; i0 < p.num_tokens; i0 += kAhead * kRopeThreads) {
+        int64_t slot[kAhead], before[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kRopeThreads;
+            slot[j] = i < p.num_tokens ? p.slots[i] : -1;
+            before[j] = i > 0 && i < p.num_tokens ? p.slots[i - 1] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t at = (slot[j] >> log2_bs) - first;
+            if (slot[j] < 0 || at < 0 || at >= blocks ||
+                (before[j] == slot[j] - 1 && (slot[j] & (p.block_size - 1)) != 0))
+                continue;
+            const uint32_t bit = 1u << (at & 31);
+            if (!(atomicOr(&seen[at >> 5], bit) & bit))
+                continue;
+            const int64_t pos = p.rotary > 0 ? p.positions[i0 + j * kRopeThreads] : 0;
+            if (pos >= 0 && (p.rotary == 0 || pos < p.max_position))
+                atomicOr(p.err, PA_DEVERR_SLOT);
+        }
     }
 }
 
-// Grid: p.checkers CTAs, which look for blocks that two runs write (5 us next
-// to the others' 8 and more), then p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
+// Grid: p.checkers CTAs, which look for blocks that two runs write (the call
+// takes no longer for them), then p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
 // query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A token alone in
 // its run (a decode step) has its heads done side by side, D / 16 lanes each
 // for K and for V.  The heads of a longer run are shared out over the CTAs of
@@ -432,11 +447,11 @@ template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(const RopeParams p)
 {
     __shared__ float both[2][2];
-    __shared__ uint32_t seen[kCheckBlocks / 32];
+    extern __shared__ uint32_t seen[];
     grid_dependency_wait();
     allow_dependent_launch();
     if (int(blockIdx.x) < p.checkers) {
-        check_runs(p, int64_t(blockIdx.x) * kCheckBlocks, seen);
+        check_runs(p, int64_t(blockIdx.x) * p.check_blocks, seen);
         return;
     }
     const int cta = int(blockIdx.x) - p.checkers;

@@ -306,12 +306,12 @@ def test_tensors_of_another_device_or_layout_are_refused():
         call(odd, odd, x, x, kc, vc)
 
 
-@pytest.mark.parametrize("kind", ["int8", "e4m3"])
-def test_blocks_that_a_call_comes_back_to_are_recorded(kind):
+@pytest.mark.parametrize("kind,nb", [("int8", 70001), ("e4m3", 70001), ("int8", 300001)])
+def test_blocks_that_a_call_comes_back_to_are_recorded(kind, nb):
     """The 8-bit write takes a block's tokens side by side: interleaved
     sequences and slots given twice set the error bit, wherever in the pool
     they are; runs in any order, split by padding between blocks, do not."""
-    kvh, d, bs, nb = 1, 64, 8, 70001
+    kvh, d, bs = 1, 64, 8
     kc, vc = (torch.zeros((nb, kvh, bs, d), device="cuda").to(CODES[kind][0]) for _ in "kv")
     scales = torch.zeros((nb, 2, 2), device="cuda")
     binding.pa_get_last_device_error()
@@ -322,7 +322,7 @@ def test_blocks_that_a_call_comes_back_to_are_recorded(kind):
                                      torch.tensor(slots, device="cuda"))
         return binding.pa_get_last_device_error()
 
-    for base in (0, 3, 32767, 32768, 65535, 65536, nb - 3):
+    for base in (0, 3, 4094, 4095, 4096, 32767, 32768, 65534, 65535, 65536, nb - 3):
         a, b = base * bs, (base + 2) * bs
         assert recorded([a, a + 1, a + 2, b, b + 1]) == 0
         assert recorded([a, b, a + 1, b + 1]) == binding.PA_DEVERR_SLOT    # drafts of two sequences
