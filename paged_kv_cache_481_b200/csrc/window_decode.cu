@@ -142,6 +142,7 @@ pa_status window_decode(void *out, const void *q, const void *k, const void *v,
     p.scale_heads = scale_heads(num_kv_heads);
     p.bf16 = dtype == PA_BF16;
     p.scale_log2 = float(double(scale) * 1.4426950408889634);
+    p.shift = weight_shift(!eight && dtype == PA_BF16, max_context_len, window, num_sinks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.part_o = reinterpret_cast<float4 *>(ws);
     p.part_ml = reinterpret_cast<float4 *>(ws + w.ml_off);

@@ -62,10 +62,11 @@
 // that the mask hides are zeroed in V and masked in the scores.  Waits are
 // bounded; one that runs out records PA_DEVERR_TIMEOUT.
 //
-// Choices of fewer bits: the weights enter the product with V in 16 bits,
-// 2^7 times larger than the softmax's (numerator and denominator alike;
+// Choices of fewer bits: the weights enter the product with V in 16 bits.
+// fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
 // below 2^15 with the stale reference), which keeps weights down to 2^-31 of
-// the largest in fp16.  With 8-bit codes the products are fp16 (codes are
+// the largest.  bf16: small enough for the largest V (weight_shift in
+// window_host.cuh).  With 8-bit codes the products are fp16 (codes are
 // exact in it): the query row is scaled by a power of two so that its largest
 // component is near 2^14, exact for every component above 2^-28 of it; a
 // block's s_v is folded into its weights relative to a running power of two
@@ -98,6 +99,7 @@ struct WindowDecodeParams {
     int log2_bs, num_blocks, scale_heads;
     int bf16;                   // type of q and out
     float scale_log2;           // softmax scale * log2(e)
+    float shift;                // weights are 2^shift times the softmax's
     float4 *part_o;             // [kWdSlots][kNq][D / 16][32 lanes]
     float4 *part_ml;            // [kWdSlots][kNq][4] (m, l) of two query heads
     unsigned *tickets;          // [units]
@@ -108,7 +110,6 @@ constexpr int kWdWarps = 4;
 constexpr int kWdThreads = kWdWarps * 32;
 constexpr int kWdMaxCtas = 512;
 constexpr int kWdMaxRanges = kWdMaxCtas * kWdWarps;
-constexpr float kWdShift = 7.0f;     // weights are 2^7 times the softmax's
 constexpr float kWdRescale = 8.0f;   // move the reference only past this growth
 constexpr int kWdSnap = 2;           // cuts of ranges this close to a unit's end move there
 constexpr int kWdMuchWork = 16;      // tiles a warp below which ranges are not worth it
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
             for (int nq = 0; nq < kNq; ++nq)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    z[nq][e] = (m[nq][e] == -INFINITY ? 0.0f : m[nq][e]) - kWdShift;
+                    z[nq][e] = (m[nq][e] == -INFINITY ? 0.0f : m[nq][e]) - p.shift;
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
                 uint32_t pb[kNq][2];
@@ -913,12 +914,22 @@ __global__ void __launch_bounds__(kWdThreads, 3)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     l[nq][e] += __shfl_xor_sync(kFullMask, l[nq][e], off);
-            if constexpr (kEight)
+            if constexpr (kEight) {
+                // up to 2^30 weights of up to 2^15: a large s_v finds room for
+                // their sum under a reference that is larger by as much
+                const bool huge = sv_ref > 0x1p64f;
+                const float down = huge ? 0x1p-45f : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l[nq][e] *= down;
+                    m[nq][e] += huge ? 45.0f : 0.0f;
+                }
 #pragma unroll
                 for (int n = 0; n < kDt; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        o[nq][n][e] *= sv_ref;
+                        o[nq][n][e] *= down * sv_ref;
+            }
         }
         // 16 dims of 8 query heads, from fragment to rows of out
         const bool bf = kEight ? p.bf16 != 0 : W::kBf16;

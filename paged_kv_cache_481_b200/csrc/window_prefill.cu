@@ -110,6 +110,7 @@ extern "C" pa_status pa_prefill_window(void *out, const void *q, const void *k_c
     p.num_blocks = num_blocks;
     p.num_rows = num_tokens;
     p.scale_log2 = float(double(scale) * 1.4426950408889634);
+    p.shift = weight_shift(dtype == PA_BF16, max_context_len, window, num_sinks);
     p.err = device_error_word();
     if (!p.err)
         return PA_ERR_CUDA;

@@ -48,8 +48,9 @@
 // flight are drained.
 //
 // Choices of fewer bits: P enters the product with V in the cache's 16-bit
-// type, 2^7 times larger than the softmax's weights (below 2^15 with the
-// stale reference), which keeps weights down to 2^-31 of the largest in fp16.
+// type.  fp16: 2^7 times larger than the softmax's weights (below 2^15 with
+// the stale reference), which keeps weights down to 2^-31 of the largest.
+// bf16: small enough for the largest V (weight_shift in window_host.cuh).
 // The row sums are taken from the unrounded weights.
 #pragma once
 
@@ -73,6 +74,7 @@ struct WindowPrefillParams {
     int num_seqs, heads, kv_heads, group, tq;
     int log2_bs, num_blocks, num_rows;
     float scale_log2;             // softmax scale * log2(e), > 0
+    float shift;                  // weights are 2^shift times the softmax's
     unsigned int *err;
 };
 
@@ -89,7 +91,6 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = (kMmaWarp + kTiles) * 32;
 constexpr uint32_t kTmemCols = 512, kTmemO = 2 * kN;
 constexpr float kRescaleLog2 = 8.0f;  // move the reference only past this growth
-constexpr float kShift = 7.0f;        // weights are 2^7 times the softmax's
 constexpr float kFloor = -1e30f;      // reference of a row that has seen nothing yet
 
 template <int D>
@@ -630,7 +631,7 @@ __device__ __forceinline__ void softmax_role(const WindowPrefillParams &p, Share
                 // moved and they are taken again.
                 float sum, largest;
                 for (;;) {
-                    write_weights<kBf16>(tS + uint32_t(buf) * kHalf, row, c, m_ref - kShift, sum, largest);
+                    write_weights<kBf16>(tS + uint32_t(buf) * kHalf, row, c, m_ref - p.shift, sum, largest);
                     const float m_new = fmaxf(m_ref, largest * c);
                     if (!__any_sync(kFullMask, m_new > m_ref + kRescaleLog2))
                         break;

@@ -181,3 +181,47 @@ def test_whole_context_agrees_with_pa_decode():
                       binding.new_workspace(4, 8, 128, 2000))
     check_decode(paged, q, out, 2000, 0, 0.1)
     check_decode(paged, q, old, 2000, 0, 0.1)
+
+
+@pytest.mark.parametrize("codes", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("lens,heads,kvh,d", [([1, 40, 700, 5000], 8, 2, 128), ([300] * 40, 20, 10, 64),
+                                              ([9000], 32, 2, 128), ([77, 0, 900], 5, 5, 64)])
+def test_values_as_large_as_the_type_holds(codes, lens, heads, kvh, d):
+    """bf16 values of half the type's largest, with one sign or both: their
+    weighted mean is representable, and no sum on the way may leave fp32."""
+    paged = Paged(lens, kvh, d, 16, BF16, seed=51, codes=codes)
+    half = torch.finfo(BF16).max / 2
+    for signs in (1, 2):
+        if codes is None:
+            nan = paged.v.isnan()
+            v = torch.rand(paged.v.shape, generator=paged.gen, device="cuda") + 1.0      # [1, 2]
+            v = v * (torch.sign(paged.v.float()) if signs == 2 else 1.0) * (half / 2)
+            paged.v = v.to(BF16).masked_fill(nan, float("nan"))
+        else:
+            if signs == 1:
+                v = paged.v.float().abs()
+                paged.v = v.to(paged.v.dtype)
+            top = float(paged.v.float().nan_to_num(0).abs().max())
+            s = torch.rand(paged.scales.shape[:2], generator=paged.gen, device="cuda") + 1.0
+            paged.scales[..., 1] = s * (half / top / 2)
+        q = paged.randn((len(lens), heads, d)) * 2
+        out = decode(paged, q, 6000, 3, d ** -0.5)
+        assert binding.pa_get_last_device_error() == 0
+        check_decode(paged, q, out, 6000, 3, d ** -0.5)
+
+
+@pytest.mark.parametrize("codes", [None, "int8"])
+def test_values_of_very_different_size_in_one_context(codes):
+    """The parts of a split context hold values of 2^-90, 1 and 2^100: each
+    part's sums are joined at their own size."""
+    paged = Paged([12000], 2, 128, 16, BF16, seed=53, codes=codes)
+    block = torch.from_numpy(paged.tables[0]).long().cuda()
+    for lo, hi, size in ((0, 250, 2.0 ** -90), (250, 500, 1.0), (500, 750, 2.0 ** 100)):
+        if codes is None:
+            paged.v[block[lo:hi]] *= size
+        else:
+            paged.scales[block[lo:hi], :, 1] *= size
+    q = paged.randn((1, 8, 128))
+    check_decode(paged, q, decode(paged, q, 12000, 0, 0.09), 12000, 0, 0.09)
+    for window, sinks in ((8000, 0), (4000, 0), (1, 4000)):     # without the smallest, the two smaller, the largest
+        check_decode(paged, q, decode(paged, q, window, sinks, 0.09), window, sinks, 0.09)

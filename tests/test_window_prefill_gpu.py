@@ -256,3 +256,19 @@ def test_how_far_a_row_that_is_not_finite_reaches(dtype, heads, kvh, window, sin
     ref, mass = attend64(q, k, v, pos.tolist(), window, sinks, 0.125)
     bound = attention_bound(ref, mass, dtype, dtype, float(v.abs().max()), length)
     assert bool(((out.double() - ref).abs() <= bound)[far.cuda()].all())
+
+
+@pytest.mark.parametrize("lens,news,heads,kvh,d", [([1, 700, 300], [1, 260, 300], 8, 2, 128),
+                                                   ([3000], [40], 5, 5, 64)])
+def test_values_as_large_as_the_type_holds(lens, news, heads, kvh, d):
+    """bf16 values of half the type's largest, with one sign or both: their
+    weighted mean is representable, and no sum on the way may leave fp32."""
+    paged = Paged(lens, kvh, d, 16, BF16, seed=51)
+    nan, sign = paged.v.isnan(), torch.sign(paged.v.float())
+    for signs in (sign.abs(), sign):
+        v = torch.rand(paged.v.shape, generator=paged.gen, device="cuda") + 1.0          # [1, 2]
+        paged.v = (v * signs * (torch.finfo(BF16).max / 4)).to(BF16).masked_fill(nan, float("nan"))
+        q = paged.randn((sum(news), heads, d)) * 2
+        out = _prefill(paged, q, news, 2500, 3, d ** -0.5)
+        assert binding.pa_get_last_device_error() == 0
+        _check(paged, q, out, news, 2500, 3, d ** -0.5)
