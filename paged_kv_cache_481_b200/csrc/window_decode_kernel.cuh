@@ -62,8 +62,12 @@
 // that the mask hides are zeroed in V and masked in the scores.  Waits are
 // bounded; one that runs out records PA_DEVERR_TIMEOUT.
 //
-// Choices of fewer bits: the weights enter the product with V in 16 bits.
-// fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
+// Choices of fewer bits: the weights enter the product with V as two 16-bit
+// numbers, the nearest one and what it leaves, within 2^-16 (bf16) or 2^-22
+// (fp16) of fp32 ones, in two matrix products.  (One alone rounds weights by
+// 2^-8, for 0 to 3 % less time: 91.0 us against 91.9 on the 32 windows, 629
+// against 633 on the 256, 20.6 against 21.2 on 4 contexts of 17 to 2047 in 8
+// bits, where the wait is for the ring otherwise.)  fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
 // below 2^15 with the stale reference), which keeps weights down to 2^-31 of
 // the largest.  bf16: small enough for the largest V (weight_shift in
 // window_host.cuh).  With 8-bit codes the products are fp16 (codes are
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                     z[nq][e] = (m[nq][e] == -INFINITY ? 0.0f : m[nq][e]) - p.shift;
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
-                uint32_t pb[kNq][2];
+                uint32_t pb[kNq][2], pr[kNq][2];  // weights, and what their rounding left
 #pragma unroll
                 for (int nq = 0; nq < kNq; ++nq)
 #pragma unroll
@@ -867,7 +871,10 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                             w0 *= ratio[mt][high];
                             w1 *= ratio[mt][high];
                         }
-                        pb[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0, w1));
+                        const uint32_t near = Half16<W::kBf16>::pack(w0, w1);
+                        const float2 x = Half16<W::kBf16>::unpack(near);
+                        pb[nq][high] = movmatrix_trans(near);
+                        pr[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0 - x.x, w1 - x.y));
                     }
                 if constexpr (!kEight) {
                     const uint32_t base = vt + W::at(16 * mt + (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
@@ -876,8 +883,10 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                         uint32_t a[4];
                         ldmatrix_x4_trans((base ^ uint32_t((n & 3) * 32)) + uint32_t(n >> 2) * 1024u, a);
 #pragma unroll
-                        for (int nq = 0; nq < kNq; ++nq)
+                        for (int nq = 0; nq < kNq; ++nq) {
                             mma16816<W::kBf16>(o[nq][n], a, pb[nq][0], pb[nq][1]);
+                            mma16816<W::kBf16>(o[nq][n], a, pr[nq][0], pr[nq][1]);
+                        }
                     }
                 } else {
                     // lane (g, c): codes of tokens 4c .. 4c + 3 of dims g and g + 8
@@ -893,8 +902,10 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                             widen4<kE4m3>(w[2 * e], a[0], a[2]);
                             widen4<kE4m3>(w[2 * e + 1], a[1], a[3]);
 #pragma unroll
-                            for (int nq = 0; nq < kNq; ++nq)
+                            for (int nq = 0; nq < kNq; ++nq) {
                                 mma16816<false>(o[nq][2 * n + e], a, pb[nq][0], pb[nq][1]);
+                                mma16816<false>(o[nq][2 * n + e], a, pr[nq][0], pr[nq][1]);
+                            }
                         }
                     }
                 }

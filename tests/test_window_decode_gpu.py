@@ -225,3 +225,38 @@ def test_values_of_very_different_size_in_one_context(codes):
     check_decode(paged, q, decode(paged, q, 12000, 0, 0.09), 12000, 0, 0.09)
     for window, sinks in ((8000, 0), (4000, 0), (1, 4000)):     # without the smallest, the two smaller, the largest
         check_decode(paged, q, decode(paged, q, window, sinks, 0.09), window, sinks, 0.09)
+
+
+@pytest.mark.parametrize("dtype,codes", STORES)
+@pytest.mark.parametrize("n,heads,kvh,d", [(2, 2, 2, 64), (6, 8, 1, 128), (33, 32, 2, 128), (6, 4, 4, 128)])
+def test_weights_keep_more_than_16_bits(dtype, codes, n, heads, kvh, d):
+    """Scores that are exact and V rows that nearly cancel, so that what is
+    left shows the weights' rounding and not the result's.
+    A score is one fp32 rounding (of at most 5.5: 2^-22) and that of
+    log2(e) (as much) off, an exponential 2^-22, the sums of up to 33 terms a
+    few 2^-24: under 2^-19 of the mass together; the weights' pair 2^-16 (bf16)
+    or 2^-22 (fp16, and 8 bits, whose s_v adds two roundings of 2^-24)."""
+    from window_helpers import attend64, half_step
+    paged = Paged([n], kvh, d, 16, dtype, seed=n + d, codes=codes)
+    t, block = torch.arange(n), torch.from_numpy(paged.tables[0]).long()
+    at = (block[t // 16].cuda(), slice(None), (t % 16).cuda())
+    row = torch.zeros((n, kvh, d), device="cuda")
+    row[..., 0] = torch.randint(0, 16, (n, kvh), generator=paged.gen, device="cuda").float()
+    unit = 1.0 if codes else 0.25
+    paged.k[at] = (row * unit).to(paged.k.dtype)
+    # signs that take turns, magnitudes alike
+    v = (torch.arange(n, device="cuda") % 2 * 2.0 - 1.0)[:, None, None] * torch.randint(
+        60, 65, (n, kvh, d), generator=paged.gen, device="cuda")
+    paged.v[at] = (v if codes else v / 64).to(paged.v.dtype)
+    if codes:
+        paged.scales[..., 0] = 0.25
+    q = torch.zeros((1, heads, d), dtype=dtype, device="cuda")
+    q[0, :, 0] = (torch.arange(heads) % 8 + 1).cuda() / 8
+    out = decode(paged, q, n, 0, 1.0)
+    k64, v64 = paged.context64(0)
+    ref, mass = attend64(q, k64, v64, [n - 1], n, 0, 1.0)
+    pair = 2.0 ** -16 if dtype == BF16 and codes is None else 2.0 ** -21
+    inner = (pair + 2.0 ** -19) * mass + n * 2.0 ** -32 * float(v64.abs().max())
+    bound = inner + half_step(dtype) * (ref.abs() + inner) + torch.finfo(dtype).smallest_normal
+    err = (out.double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
