@@ -98,7 +98,8 @@ PA_API pa_status pa_rope_and_cache(void *q_out, int64_t q_out_stride, const void
  *     s = m / top                     when the new rows start at row 0,
  *     s = max(the block's s, m / top) otherwise; where s grows, the older
  *                                     rows become round(code * (s_old / s)).
- * (Where s is new, x / s is taken as x top / m, before s is rounded to fp32.)
+ * (Where s is new, x / s is taken as x top / m, before s is rounded to fp32;
+ * so too where s lies below the normal numbers and x / s would pass the top.)
  * Rows behind the new ones keep their codes (a later write replaces them).
  * A block whose rows are all zero has s = 0 and codes 0.  Rows holding inf or
  * NaN make their block's values unspecified.  A block is written by one run

@@ -220,9 +220,12 @@ struct CodeScale {
         scale = __fdiv_rn(m, top);
         grown = first == 0 || scale > old;
         scale = grown ? scale : old;
-        d = grown ? m : old;
+        // (a scale below the normal numbers may be rounded so far down that
+        // x / s passes the top: such rows take x top / m too)
+        const bool by_max = grown || (old < 0x1p-126f && m > __fmul_rn(old, top));
+        d = by_max ? m : old;
         const float by = d > 1e30f ? 0x1p-40f : d < 1e-30f ? 0x1p40f : 1.0f;
-        a = grown ? top * by : by;
+        a = by_max ? top * by : by;
         d *= by;
         r = d > 0.0f ? __frcp_rn(d) : 0.0f;   // all codes are 0 where the scale is
     }

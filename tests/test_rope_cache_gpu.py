@@ -1,6 +1,8 @@
 """The rotating cache writes against their 64-bit form: both rotations, both
 16-bit types, strided and padded rows, neighbours left alone, and the 8-bit
 cache's scales as its blocks fill up."""
+import math
+
 import pytest
 import torch
 
@@ -340,3 +342,33 @@ def test_blocks_that_a_call_comes_back_to_are_recorded(kind, nb):
     first = torch.tensor([r[0] % bs for r in runs[8:-1]], device="cuda")
     got = codes[torch.arange(len(first), device="cuda"), 0, first, 0] * scale
     assert bool(((got - 1).abs() < 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_scales_below_the_normal_numbers(kind):
+    """Rotated keys so small that the scale itself is a few times 2^-149: a
+    later row that does not raise the rounded scale still has codes of its own
+    sign up to the top."""
+    code_type, top = CODES[kind]
+    d, bs = 64, 8
+    kc, vc = (torch.zeros((1, 1, bs, d), device="cuda").to(code_type) for _ in "kv")
+    scales = torch.zeros((1, 2, 2), device="cuda")
+    # keys of 2^-133 (bf16's smallest) turned by a table whose cosines make them
+    # `units` times 2^-149 and whose sines are zero
+    units = [int(top * 0.8), int(top * 1.4), -int(top * 1.45), int(top * 0.5), -int(top * 1.49)]
+    table = torch.zeros((len(units), d), device="cuda")
+    table[:, :d // 2] = torch.tensor(units, device="cuda")[:, None].float() * 2.0 ** -16
+    k = torch.full((1, 1, d), 2.0 ** -133, dtype=BF16, device="cuda")
+    v = torch.ones((1, 1, d), dtype=BF16, device="cuda")
+    for i, u in enumerate(units):
+        binding.pa_rope_and_cache_q8(torch.empty_like(k), k, k, v, kc, vc, scales, table,
+                                     torch.tensor([i], device="cuda"), torch.tensor([i], device="cuda"))
+        assert float(scales[0, 0, 0]) == 2.0 ** -149       # |units| / top rounds to 1
+        want = max(-top, min(top, float(u)))
+        step = 0.5 if kind == "int8" else 2.0 ** -4 * abs(want)
+        got = kc[0, 0, i].float()
+        if i > 0 and abs(u) <= top:
+            assert bool(((got - want).abs() <= step).all())
+        else:                  # x top / m (the scale is new, or would pass the top)
+            assert bool((got == math.copysign(top, u)).all())
+    assert bool((vc[0, 0, :len(units)].float() == top).all())
