@@ -86,7 +86,7 @@
 #include "half_types.cuh"
 #include "mma_sync.cuh"
 #include "ptx.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_window.cuh"
 
 namespace pa {
 
