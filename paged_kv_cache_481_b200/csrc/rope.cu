@@ -67,20 +67,20 @@ pa_status rope_params(pa::RopeParams &p, void *q_out, int64_t q_out_stride, cons
     return p.err ? PA_OK : PA_ERR_CUDA;
 }
 
-template <int D, bool kBf16, bool kInterleaved, int kPasses>
+template <int D, bool kBf16, bool kInterleaved>
 cudaError_t launch_rope(const pa::RopeParams &p, cudaStream_t stream)
 {
     const int rows = p.num_heads + 2 * p.num_kv_heads;
-    const int per_cta = pa::kRopeThreads / (D / 16) * kPasses;
+    const int per_cta = pa::kRopeThreads / (D / 16) * pa::kRopePasses;
     const dim3 grid(unsigned(p.num_tokens), unsigned((rows + per_cta - 1) / per_cta));
-    return launch_pdl(pa::rope_and_cache_kernel<D, kBf16, kInterleaved, kPasses>, grid,
+    return launch_pdl(pa::rope_and_cache_kernel<D, kBf16, kInterleaved>, grid,
                       dim3(pa::kRopeThreads), 0, stream, p);
 }
 
 template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 cudaError_t launch_rope_q8(pa::RopeParams p, cudaStream_t stream)
 {
-    constexpr int kRows = pa::kRopeThreads / (D / 16) * 2, kSpan = 2 * 32 / (D / 16);
+    constexpr int kRows = pa::kRopeThreads / (D / 16) * pa::kRopePasses, kSpan = 2 * 32 / (D / 16);
     p.groups = std::max((p.num_heads + kRows - 1) / kRows, (p.num_kv_heads + kSpan - 1) / kSpan);
     p.check_blocks = p.num_blocks <= pa::kCheckFew * pa::kCheckParts ? pa::kCheckFew : pa::kCheckMany;
     p.checkers = p.num_tokens > 1 ? 1 + (p.num_blocks - 1) / p.check_blocks : 0;
@@ -113,7 +113,7 @@ pa_status pa_rope_and_cache(void *q_out, int64_t q_out_stride, const void *q, in
     const cudaError_t e = with_bool(head_dim == 128, [&](auto d128) {
         return with_bool(dtype == PA_BF16, [&](auto bf16) {
             return with_bool(interleaved != 0, [&](auto inter) {
-                return launch_rope<d128 ? 128 : 64, bf16, inter, 2>(
+                return launch_rope<d128 ? 128 : 64, bf16, inter>(
                     p, reinterpret_cast<cudaStream_t>(stream));
             });
         });

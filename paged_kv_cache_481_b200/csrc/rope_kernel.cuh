@@ -132,15 +132,16 @@ __device__ __forceinline__ bool token_is_live(const RopeParams &p, bool report, 
 }
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopePasses = 2;     // rows of a token that a thread works on
 
-// Rows [row0, row0 + kPasses * rows per pass) of one token: row r < H is
+// Rows [row0, row0 + kRopePasses * rows per pass) of one token: row r < H is
 // query head r, then the K heads, then the V heads.  The rows are fetched
 // together with the token's slot and position, so that only the angles wait
 // for another load.
-template <int D, bool kBf16, bool kInterleaved, int kPasses, bool kQueriesOnly, int kThreads>
+template <int D, bool kBf16, bool kInterleaved, bool kQueriesOnly>
 __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0)
 {
-    constexpr int kUnits = D / 16, kRows = kThreads / kUnits;
+    constexpr int kUnits = D / 16, kRows = kRopeThreads / kUnits;
     const int u = threadIdx.x % kUnits, r0 = row0 + threadIdx.x / kUnits;
     const int H = p.num_heads, KVH = p.num_kv_heads;
     const int rows = kQueriesOnly ? H : H + 2 * KVH;
@@ -148,9 +149,9 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0)
     int p0, p1;
     unit_pieces<kInterleaved>(u, p.rotary, p0, p1);
     const int64_t slot = p.slots[i], pos = p.rotary > 0 ? p.positions[i] : 0;
-    uint4 v0[kPasses], v1[kPasses];
+    uint4 v0[kRopePasses], v1[kRopePasses];
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
+    for (int k = 0; k < kRopePasses; ++k) {
         const int r = r0 + k * kRows;
         if (r >= rows)
             continue;
@@ -171,7 +172,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0)
         load_angles(a, p.cos_sin + pos * p.rotary, p.rotary / 2, u);
     const int64_t block = slot / p.block_size, offset = slot % p.block_size;
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
+    for (int k = 0; k < kRopePasses; ++k) {
         const int r = r0 + k * kRows;
         if (r >= rows)
             continue;
@@ -191,14 +192,14 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, int i, int row0)
     }
 }
 
-// Grid (num_tokens, ceil(rows / (kPasses * rows per pass))).
-template <int D, bool kBf16, bool kInterleaved, int kPasses>
+// Grid (num_tokens, ceil(rows / (kRopePasses * rows per pass))).
+template <int D, bool kBf16, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const RopeParams p)
 {
     grid_dependency_wait();
     allow_dependent_launch();
-    constexpr int kRows = kRopeThreads / (D / 16) * kPasses;
-    rope_rows<D, kBf16, kInterleaved, kPasses, false, kRopeThreads>(p, blockIdx.x, blockIdx.y * kRows);
+    constexpr int kRows = kRopeThreads / (D / 16) * kRopePasses;
+    rope_rows<D, kBf16, kInterleaved, false>(p, blockIdx.x, blockIdx.y * kRows);
 }
 
 // ------------------------------------------------------- 8-bit block cache
@@ -459,14 +460,14 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(cons
     }
     const int cta = int(blockIdx.x) - p.checkers;
     constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kSpan = 2 * kHeads;
-    constexpr int kPasses = 2, kRows = kRopeThreads / kUnits * kPasses;
+    constexpr int kRows = kRopeThreads / kUnits * kRopePasses;
     const int i = cta / p.groups, g = cta % p.groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     // slots of the kSpan tokens before this one and of those from it on
     const int j = i - kSpan + lane;
     const int64_t near = j >= 0 && j < p.num_tokens ? p.slots[j] : -1;
     if (g * kRows < p.num_heads)
-        rope_rows<D, kBf16, kInterleaved, kPasses, true, kRopeThreads>(p, i, g * kRows);
+        rope_rows<D, kBf16, kInterleaved, true>(p, i, g * kRows);
     const int h0 = g * kSpan;
     if (h0 >= p.num_kv_heads)
         return;

@@ -517,7 +517,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&r)[kHalf])
     for (int i = 0; i < kHalf; i += 8)
 #pragma unroll
         for (int a = 0; a < 4; ++a)
-            m[a] = max3f(m[a], __uint_as_float(r[i + 2 * a]), __uint_as_float(r[i + 2 * a + 1]));
+            m[a] = max3_f32(m[a], __uint_as_float(r[i + 2 * a]), __uint_as_float(r[i + 2 * a + 1]));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -542,7 +542,7 @@ __device__ __forceinline__ void write_weights(uint32_t tS, const uint32_t (&r)[k
             const float p0 = exp2_sfu(v.x), p1 = exp2_sfu(v.y);
             total[e & 1] = add_f32x2(total[e & 1], pack_f32x2(p0, p1));
             pk[i] = Half16<kBf16>::pack(p0, p1);
-            top[e & 1] = max3f(top[e & 1], __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+            top[e & 1] = max3_f32(top[e & 1], __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
         tmem_store16(tS + uint32_t(part * (kHalf / 4)), pk);
     }
