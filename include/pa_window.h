@@ -137,7 +137,7 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
  *     out[b, h, :] = sum_t exp(s_t - max s) V_t / sum_t exp(s_t - max s),
  *     s_t = scale * sum_d q[b, h, d] * K_t[d],  over the positions t it sees.
  * Scores, softmax statistics and sums are fp32; the weights enter the product
- * with V as two numbers of the cache's 16-bit type (2^-16 of fp32's value or
+ * with V as two numbers of the cache's 16-bit type (2^-15 of fp32's value or
  * better together).  L == 0 writes zeros.  What positions
  * that are not seen hold has no effect.  max_context_len bounds
  * context_lens and must not exceed max_blocks_per_seq * block_size or 2^30.  Results

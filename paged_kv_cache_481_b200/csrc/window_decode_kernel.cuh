@@ -62,12 +62,12 @@
 // that the mask hides are zeroed in V and masked in the scores.  Waits are
 // bounded; one that runs out records PA_DEVERR_TIMEOUT.
 //
-// Choices of fewer bits: the weights enter the product with V as two 16-bit
-// numbers, the nearest one and what it leaves, within 2^-16 (bf16) or 2^-22
-// (fp16) of fp32 ones, in two matrix products.  (One alone rounds weights by
-// 2^-8, for 0 to 3 % less time: 91.0 us against 91.9 on the 32 windows, 629
-// against 633 on the 256, 20.6 against 21.2 on 4 contexts of 17 to 2047 in 8
-// bits, where the wait is for the ring otherwise.)  fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
+// Choices of fewer bits: the weights enter the product with V as the sum of
+// two 16-bit numbers, within 2^-15 (bf16) or 2^-20 (fp16) of fp32 ones, in two
+// matrix products.  (One alone rounds weights by
+// 2^-8, for 0 to 4 % less time: 90.4 us against 91.0 on the 32 windows, 629
+// against 635 on the 256, 19.8 against 20.6 on 4 contexts of 17 to 2047 in 8
+// bits; the large 8-bit batch takes 1 % less with two.)  fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
 // below 2^15 with the stale reference), which keeps weights down to 2^-31 of
 // the largest.  bf16: small enough for the largest V (weight_shift in
 // window_host.cuh).  With 8-bit codes the products are fp16 (codes are
@@ -300,6 +300,24 @@ __device__ __forceinline__ float pow2_at_least(float x)
     return __uint_as_float((__float_as_uint(x) + 0x7fffffu) & 0x7f800000u);
 }
 
+
+// The larger one of the two 16-bit numbers that stand for a weight.  Of 8-bit
+// codes, which are finite, the nearest; else less than the weight, so that the
+// rest is not zero or negative and an infinite V row stays infinite: bf16, the
+// number at or below the next smaller fp32 one (the rest is rounded by 2^-15 of
+// the weight); fp16, a little less than the nearest one (2^-20; weights below
+// 2^-23 have one part only).
+template <KvStore kStore>
+__device__ __forceinline__ uint32_t most_of(float w0, float w1)
+{
+    if constexpr (kStore == KvStore::kBf16)
+        return __byte_perm(max(__float_as_uint(w0), 1u) - 1u, max(__float_as_uint(w1), 1u) - 1u, 0x7632);
+    else if constexpr (kStore == KvStore::kF16)
+        return Half16<false>::pack(fmaxf(fmaf(w0, 1.0f - 0x1p-10f, -0x1p-24f), 0.0f),
+                                   fmaxf(fmaf(w1, 1.0f - 0x1p-10f, -0x1p-24f), 0.0f));
+    else
+        return Half16<false>::pack(w0, w1);
+}
 
 // Joins a unit's parts, in order: for each 8 query heads the fragments n0,
 // n0 + kStride, ... (kCount of them), kAhead parts' loads in flight.
@@ -858,7 +876,7 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                     z[nq][e] = (m[nq][e] == -INFINITY ? 0.0f : m[nq][e]) - p.shift;
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt) {
-                uint32_t pb[kNq][2], pr[kNq][2];  // weights, and what their rounding left
+                uint32_t pb[kNq][2], pr[kNq][2];  // most of the weights, and the rest
 #pragma unroll
                 for (int nq = 0; nq < kNq; ++nq)
 #pragma unroll
@@ -871,9 +889,9 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                             w0 *= ratio[mt][high];
                             w1 *= ratio[mt][high];
                         }
-                        const uint32_t near = Half16<W::kBf16>::pack(w0, w1);
-                        const float2 x = Half16<W::kBf16>::unpack(near);
-                        pb[nq][high] = movmatrix_trans(near);
+                        const uint32_t most = most_of<kStore>(w0, w1);
+                        const float2 x = Half16<W::kBf16>::unpack(most);
+                        pb[nq][high] = movmatrix_trans(most);
                         pr[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0 - x.x, w1 - x.y));
                     }
                 if constexpr (!kEight) {

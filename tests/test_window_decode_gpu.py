@@ -234,8 +234,10 @@ def test_weights_keep_more_than_16_bits(dtype, codes, n, heads, kvh, d):
     left shows the weights' rounding and not the result's.
     A score is one fp32 rounding (of at most 5.5: 2^-22) and that of
     log2(e) (as much) off, an exponential 2^-22, the sums of up to 33 terms a
-    few 2^-24: under 2^-19 of the mass together; the weights' pair 2^-16 (bf16)
-    or 2^-22 (fp16, and 8 bits, whose s_v adds two roundings of 2^-24)."""
+    few 2^-24: under 2^-19 of the mass together.  Of the weights' pair the
+    second is rounded: below 2^-7 of the weight by 2^-8 of it in bf16, 2^-15;
+    up to 1.5 2^-10 by 2^-11 in fp16, under 2^-20 (8 bits: 2^-22, and two
+    roundings of 2^-24 that s_v adds)."""
     from window_helpers import attend64, half_step
     paged = Paged([n], kvh, d, 16, dtype, seed=n + d, codes=codes)
     t, block = torch.arange(n), torch.from_numpy(paged.tables[0]).long()
@@ -255,8 +257,23 @@ def test_weights_keep_more_than_16_bits(dtype, codes, n, heads, kvh, d):
     out = decode(paged, q, n, 0, 1.0)
     k64, v64 = paged.context64(0)
     ref, mass = attend64(q, k64, v64, [n - 1], n, 0, 1.0)
-    pair = 2.0 ** -16 if dtype == BF16 and codes is None else 2.0 ** -21
+    pair = 2.0 ** -15 if dtype == BF16 and codes is None else 2.0 ** -20
     inner = (pair + 2.0 ** -19) * mass + n * 2.0 ** -32 * float(v64.abs().max())
     bound = inner + half_step(dtype) * (ref.abs() + inner) + torch.finfo(dtype).smallest_normal
     err = (out.double() - ref).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size", [0.0, 0.3])
+def test_infinite_values_that_are_seen_stay_infinite(dtype, size):
+    """One dim of V is infinite in one visible row: that dim of the result is
+    that infinity (the weight is positive), the others are what they were.
+    Equal scores (size 0) have weights of few bits, others of all."""
+    paged = Paged([700, 33, 1], 2, 64, 16, dtype, seed=71)
+    q = paged.randn((3, 8, 64)) * size
+    want = decode(paged, q, 500, 4, 0.125)
+    for b, t, dim, value in ((0, 2, 5, "inf"), (0, 650, 40, "-inf"), (1, 30, 0, "inf"), (2, 0, 63, "-inf")):
+        paged.v[int(paged.tables[b, t // 16]), :, t % 16, dim] = float(value)
+        want[b, :, dim] = float(value)
+    assert torch.equal(decode(paged, q, 500, 4, 0.125), want)
