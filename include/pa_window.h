@@ -137,8 +137,10 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
  *     out[b, h, :] = sum_t exp(s_t - max s) V_t / sum_t exp(s_t - max s),
  *     s_t = scale * sum_d q[b, h, d] * K_t[d],  over the positions t it sees.
  * Scores, softmax statistics and sums are fp32; the weights enter the product
- * with V as two numbers of the cache's 16-bit type (2^-15 of fp32's value or
- * better together).  L == 0 writes zeros.  What positions
+ * with V as the sum of two numbers of the cache's 16-bit type (within 2^-15 of
+ * fp32's value), or as one where query heads are taken 16 at a time (groups of
+ * more than 8, and more than 32 units of sequence, K/V head and 16 of its query
+ * heads).  L == 0 writes zeros.  What positions
  * that are not seen hold has no effect.  max_context_len bounds
  * context_lens and must not exceed max_blocks_per_seq * block_size or 2^30.  Results
  * do not depend on the order in which blocks of threads run.
@@ -154,8 +156,8 @@ PA_API pa_status pa_decode_window(void *out, const void *q, const void *k_cache,
 /*
  * pa_decode_window over the 8-bit cache: K_t = s_k * code, V_t = s_v * code
  * with the scales of the block and head that hold t; q and out in `dtype`.  The
- * weights enter the product with V times s_v, as two fp16 numbers relative to
- * the largest: what is below 2^-31 of it is lost.
+ * weights enter the product with V times s_v, in fp16 numbers (as many as
+ * there) relative to the largest: what is below 2^-31 of it is lost.
  * About half the bytes of pa_decode_window.
  */
 PA_API pa_status pa_decode_q8(void *out, const void *q, const void *k_codes, const void *v_codes,

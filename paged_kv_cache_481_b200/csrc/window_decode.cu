@@ -25,11 +25,14 @@ struct WindowWorkspace {
     size_t ml_off, ticket_off, total;
 };
 
-// Query heads of a unit: 8, or 16 for larger groups when that leaves units
-// enough (both sides measured in window_decode_kernel.cuh).
+// Query heads of a unit: 4 for groups of up to 4, else 8, or 16 for groups of
+// more than 8 when that leaves units enough (measured in
+// window_decode_kernel.cuh).
 int unit_heads(int num_seqs, int num_kv_heads, int group)
 {
     constexpr int64_t kFewUnits = 32;
+    if (group <= 4)
+        return 4;
     return group <= 8 || int64_t(num_seqs) * num_kv_heads * ((group + 15) / 16) <= kFewUnits ? 8 : 16;
 }
 
@@ -45,12 +48,12 @@ WindowWorkspace window_workspace(int num_seqs, int num_heads, int num_kv_heads)
     return w;
 }
 
-template <pa::KvStore kStore, int D, int kNq>
+template <pa::KvStore kStore, int D, int kHeads>
 pa_status launch_window(const pa::WindowDecodeParams &p, const void *k, const void *v,
                         cudaStream_t stream)
 {
     using W = pa::WindowTraits<kStore, D>;
-    constexpr auto kernel = pa::window_decode_kernel<kStore, D, kNq>;
+    constexpr auto kernel = pa::window_decode_kernel<kStore, D, kHeads>;
     static std::atomic<int> grid_for[kMaxDevices];  // 0 = not configured yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -152,14 +155,17 @@ pa_status window_decode(void *out, const void *q, const void *k, const void *v,
         return PA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return with_bool(head_dim == 128, [&](auto d128) {
-        return with_bool(per == 16, [&](auto many) {
-            constexpr int D = d128 ? 128 : 64, kNq = many ? 2 : 1;
+        auto of = [&](auto heads) {
+            constexpr int D = d128 ? 128 : 64, kHeads = heads;
             if (eight)
-                return kv_type == PA_KV8_E4M3 ? launch_window<pa::KvStore::kE4m3, D, kNq>(p, k, v, st)
-                                              : launch_window<pa::KvStore::kInt8, D, kNq>(p, k, v, st);
-            return dtype == PA_BF16 ? launch_window<pa::KvStore::kBf16, D, kNq>(p, k, v, st)
-                                    : launch_window<pa::KvStore::kF16, D, kNq>(p, k, v, st);
-        });
+                return kv_type == PA_KV8_E4M3 ? launch_window<pa::KvStore::kE4m3, D, kHeads>(p, k, v, st)
+                                              : launch_window<pa::KvStore::kInt8, D, kHeads>(p, k, v, st);
+            return dtype == PA_BF16 ? launch_window<pa::KvStore::kBf16, D, kHeads>(p, k, v, st)
+                                    : launch_window<pa::KvStore::kF16, D, kHeads>(p, k, v, st);
+        };
+        return per == 4    ? of(std::integral_constant<int, 4>{})
+               : per == 8 ? of(std::integral_constant<int, 8>{})
+                          : of(std::integral_constant<int, 16>{});
     });
 }
 

@@ -23,7 +23,7 @@
 // 60 % of the time.  Small calls are bound by latency: lengths, table, tiles,
 // then the join, 14.5 us for one sequence and a window of 4100.
 //
-// Layout of the work: a "unit" is (sequence, K/V head, 8 * kNq query heads);
+// Layout of the work: a "unit" is (sequence, K/V head, kHeads query heads);
 // its visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens
 // at D = 128 in 16 bits).  The kernel's blocks count the tiles and choose, all
 // alike, one of three ways to share them out:
@@ -50,10 +50,12 @@
 // bits 436 / 396.  8 units of 16 heads and 8000 tokens: CTAs 25, single warps
 // 57.
 //
-// kNq: groups of more than 8 heads take 16 columns at a time, which reads K
-// and V half as often (128 such units of 8000 tokens: 94 us against 119), but
-// 8 at a time when there are 32 such units or fewer, twice the parts to run
-// side by side (8 units of 8000: 20.6 us against 24.2, 32: 32.4 against 35).
+// kHeads: groups of more than 8 heads take 16 columns at a time, which reads K
+// and V half as often (128 such units of 8000 tokens: 94 us against 131, 64 to
+// 71 against 77 to 88 in 8 bits), but 8 at a time when there are 32 such units
+// or fewer, twice the parts to run side by side (8 units of 8000: 18.2 us
+// against 23.3, 32: 31.9 against 34.0; in 8 bits 17.7 and 28.3 against 25.9 and
+// 31.7).
 //
 // Each warp keeps a ring of kStages tiles full, across units: one lane per
 // block run issues TMA boxes (K and V) that complete an mbarrier, with the
@@ -63,19 +65,24 @@
 // bounded; one that runs out records PA_DEVERR_TIMEOUT.
 //
 // Choices of fewer bits: the weights enter the product with V as the sum of
-// two 16-bit numbers, within 2^-15 (bf16) or 2^-20 (fp16) of fp32 ones, in two
-// matrix products.  (One alone rounds weights by
-// 2^-8, for 0 to 4 % less time: 90.4 us against 91.0 on the 32 windows, 629
-// against 635 on the 256, 19.8 against 20.6 on 4 contexts of 17 to 2047 in 8
-// bits; the large 8-bit batch takes 1 % less with two.)  fp16: 2^7 times larger than the softmax's (numerator and denominator alike;
-// below 2^15 with the stale reference), which keeps weights down to 2^-31 of
-// the largest.  bf16: small enough for the largest V (weight_shift in
-// window_host.cuh).  With 8-bit codes the products are fp16 (codes are
-// exact in it): the query row is scaled by a power of two so that its largest
-// component is near 2^14, exact for every component above 2^-28 of it; a
-// block's s_v is folded into its weights relative to a running power of two
-// at or above the largest s_v so far (a block's values count down to 2^-31 of
-// the largest s_v times the largest weight).
+// two 16-bit numbers, within 2^-15 (bf16) or 2^-20 (fp16) of fp32 ones.  With up
+// to 4 heads the second ones stand in columns 4 to 7, which the heads of
+// columns 0 to 3 take once more; with up to 8 they are a second matrix product.
+// One number alone rounds weights by 2^-8 or 2^-11, for this much less time
+// (us): 32 windows of 40 heads 90.4 against 90.6, 256 windows in groups of 8
+// 620 against 626; in 8 bits, 4 contexts of 40 heads 19.3 against 19.7, groups
+// of 8 19.2 against 20.3 (200 contexts of 300 to 900) and 369 against 372 (the
+// 128).  With 16 heads there is one number: two would take 32 contexts of
+// 8000 in 8 bits from 65 to 77 us, and groups of 128 from 128 to 153.
+// fp16 weights are 2^7 times larger than the softmax's (numerator and
+// denominator alike; below 2^15 with the stale reference), which keeps those
+// down to 2^-31 of the largest.  bf16: small enough for the largest V
+// (weight_shift in window_host.cuh).  With 8-bit codes the products are fp16
+// (codes are exact in it): the query row is scaled by a power of two so that
+// its largest component is near 2^14, exact for every component above 2^-28 of
+// it; a block's s_v is folded into its weights relative to a running power of
+// two at or above the largest s_v so far (a block's values count down to 2^-31
+// of the largest s_v times the largest weight).
 #pragma once
 
 #include <cuda.h>
@@ -99,7 +106,7 @@ struct WindowDecodeParams {
     const int32_t *tables;      // [B, max_blocks]
     const int32_t *lens;        // [B]
     int max_blocks, max_len, window, sinks;
-    int num_seqs, heads, kv_heads, group, row_tiles;  // row_tiles = ceil(group / (8 kNq))
+    int num_seqs, heads, kv_heads, group, row_tiles;  // row_tiles = ceil(group / kHeads)
     int log2_bs, num_blocks, scale_heads;
     int bf16;                   // type of q and out
     float scale_log2;           // softmax scale * log2(e)
@@ -378,13 +385,16 @@ __device__ __forceinline__ void merge_parts(int parts, Slot slot_of, Ml part_ml,
     }
 }
 
-template <KvStore kStore, int D, int kNq>
+template <KvStore kStore, int D, int kHeads>
 __global__ void __launch_bounds__(kWdThreads, 3)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ WindowDecodeParams p)
 {
     using W = WindowTraits<kStore, D>;
     constexpr int kTile = W::kTile, kMt = W::kMt, kStages = W::kStages, kDt = D / 16;
+    constexpr int kNq = kHeads > 8 ? 2 : 1;      // eights of columns
+    constexpr bool kTwice = kHeads == 4;         // columns 4 .. 7 are heads 0 .. 3 once more
+    constexpr bool kPair = kHeads == 8;          // two products for the two parts of the weights
     constexpr bool kEight = W::kEight, kE4m3 = kStore == KvStore::kE4m3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t s_full[kWdWarps][kStages];
@@ -645,8 +655,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
     uint32_t phase = 0;
     bool have = true;
     while (have) {
-        const int h = s_seg[warp].r / p.row_tiles, row0 = (s_seg[warp].r % p.row_tiles) * (8 * kNq);
-        const int rows = min(8 * kNq, p.group - row0);
+        const int h = s_seg[warp].r / p.row_tiles, row0 = (s_seg[warp].r % p.row_tiles) * kHeads;
+        const int rows = min(kHeads, p.group - row0);
         const size_t out_row = size_t(s_seg[warp].b) * p.heads + size_t(h) * p.group + row0;
 
         // ---- query heads as the columns (B operand) ----------------------
@@ -654,8 +664,9 @@ __global__ void __launch_bounds__(kWdThreads, 3)
         float f[kNq][2];           // what the scores of columns 2c, 2c + 1 are multiplied by
 #pragma unroll
         for (int nq = 0; nq < kNq; ++nq) {
-            const bool there = 8 * nq + g < rows;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (out_row + 8 * nq + (there ? g : 0)) * D;
+            const int mine = 8 * nq + (kTwice ? g & 3 : g);
+            const bool there = mine < rows;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (out_row + (there ? mine : 0)) * D;
             if constexpr (!kEight) {
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(src) + c;
 #pragma unroll
@@ -889,10 +900,16 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                             w0 *= ratio[mt][high];
                             w1 *= ratio[mt][high];
                         }
-                        const uint32_t most = most_of<kStore>(w0, w1);
-                        const float2 x = Half16<W::kBf16>::unpack(most);
-                        pb[nq][high] = movmatrix_trans(most);
-                        pr[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0 - x.x, w1 - x.y));
+                        if constexpr (kNq == 2) {
+                            pb[nq][high] = movmatrix_trans(Half16<W::kBf16>::pack(w0, w1));
+                        } else {
+                            const uint32_t most = most_of<kStore>(w0, w1);
+                            const float2 x = Half16<W::kBf16>::unpack(most);
+                            const uint32_t rest = Half16<W::kBf16>::pack(w0 - x.x, w1 - x.y);
+                            pb[nq][high] = movmatrix_trans(kTwice && c >= 2 ? rest : most);
+                            if constexpr (kPair)
+                                pr[nq][high] = movmatrix_trans(rest);
+                        }
                     }
                 if constexpr (!kEight) {
                     const uint32_t base = vt + W::at(16 * mt + (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
@@ -903,7 +920,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
 #pragma unroll
                         for (int nq = 0; nq < kNq; ++nq) {
                             mma16816<W::kBf16>(o[nq][n], a, pb[nq][0], pb[nq][1]);
-                            mma16816<W::kBf16>(o[nq][n], a, pr[nq][0], pr[nq][1]);
+                            if constexpr (kPair)
+                                mma16816<W::kBf16>(o[nq][n], a, pr[nq][0], pr[nq][1]);
                         }
                     }
                 } else {
@@ -922,7 +940,8 @@ __global__ void __launch_bounds__(kWdThreads, 3)
 #pragma unroll
                             for (int nq = 0; nq < kNq; ++nq) {
                                 mma16816<false>(o[nq][2 * n + e], a, pb[nq][0], pb[nq][1]);
-                                mma16816<false>(o[nq][2 * n + e], a, pr[nq][0], pr[nq][1]);
+                                if constexpr (kPair)
+                                    mma16816<false>(o[nq][2 * n + e], a, pr[nq][0], pr[nq][1]);
                             }
                         }
                     }
@@ -960,6 +979,12 @@ __global__ void __launch_bounds__(kWdThreads, 3)
                         o[nq][n][e] *= down * sv_ref;
             }
         }
+        if constexpr (kTwice)
+#pragma unroll
+            for (int n = 0; n < kDt; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[0][n][e] += __shfl_xor_sync(kFullMask, o[0][n][e], 2);
         // 16 dims of 8 query heads, from fragment to rows of out
         const bool bf = kEight ? p.bf16 != 0 : W::kBf16;
         auto store = [&](int nq, int n, const float4 &v) {

@@ -228,7 +228,8 @@ def test_values_of_very_different_size_in_one_context(codes):
 
 
 @pytest.mark.parametrize("dtype,codes", STORES)
-@pytest.mark.parametrize("n,heads,kvh,d", [(2, 2, 2, 64), (6, 8, 1, 128), (33, 32, 2, 128), (6, 4, 4, 128)])
+@pytest.mark.parametrize("n,heads,kvh,d", [(2, 2, 2, 64), (6, 8, 1, 128), (33, 32, 2, 128), (6, 4, 4, 128),
+                                           (20, 9, 3, 64), (9, 6, 1, 128)])
 def test_weights_keep_more_than_16_bits(dtype, codes, n, heads, kvh, d):
     """Scores that are exact and V rows that nearly cancel, so that what is
     left shows the weights' rounding and not the result's.
@@ -266,12 +267,13 @@ def test_weights_keep_more_than_16_bits(dtype, codes, n, heads, kvh, d):
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("size", [0.0, 0.3])
-def test_infinite_values_that_are_seen_stay_infinite(dtype, size):
+@pytest.mark.parametrize("heads", [2, 6, 16, 64])
+def test_infinite_values_that_are_seen_stay_infinite(dtype, size, heads):
     """One dim of V is infinite in one visible row: that dim of the result is
     that infinity (the weight is positive), the others are what they were.
     Equal scores (size 0) have weights of few bits, others of all."""
     paged = Paged([700, 33, 1], 2, 64, 16, dtype, seed=71)
-    q = paged.randn((3, 8, 64)) * size
+    q = paged.randn((3, heads, 64)) * size
     want = decode(paged, q, 500, 4, 0.125)
     for b, t, dim, value in ((0, 2, 5, "inf"), (0, 650, 40, "-inf"), (1, 30, 0, "inf"), (2, 0, 63, "-inf")):
         paged.v[int(paged.tables[b, t // 16]), :, t % 16, dim] = float(value)
