@@ -12,12 +12,13 @@
 // hold whole pairs: elements [8u, 8u + 8) and [r/2 + 8u, ...) of a
 // half-split rotation of r dims, else 16 neighbouring elements.
 //
-// Measured (kernel alone, one B200): 9 packed prompts, H 32, KVH 8, bf16:
-// 43.6 us, 5.6 TB/s, 86 % of a plain copy's rate (the rest is the first and
-// the last wave); 32 tokens of 40 heads: 4.2 us, a launch and three dependent
-// loads.  The 8-bit write: 12 chunks, H 32, KVH 8, e4m3: 39 us, 3.6 TB/s, bound
-// by the chain slot -> rows -> angles -> maximum -> codes with 64 registers a
-// thread; 256 single tokens of 40 heads: 8.3 us.
+// Measured (kernel alone in a graph of four, one B200 at 1965 MHz): 9 packed
+// prompts, H 32, KVH 8, bf16: 42.2 us, 5.8 TB/s, 88 % of a plain copy's rate
+// (the rest is the first and the last wave); 32 tokens of 40 heads: 2.1 us,
+// three dependent loads.  The 8-bit write: 12 chunks, H 32, KVH 8, e4m3: 37.4
+// us, 3.8 TB/s, bound by the chain slot -> rows -> angles -> maximum -> codes
+// with 64 registers a thread, which are too few: all instances spill 84 to 100
+// bytes and read back 220 to 316; 256 single tokens of 40 heads: 6.2 us.
 #pragma once
 
 #include <cstdint>

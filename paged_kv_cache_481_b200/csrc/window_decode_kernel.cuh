@@ -17,11 +17,12 @@
 // once per group.  (tcgen05 needs 64 rows and more and its operands through
 // one more hop; at these sizes the copies would wait for it.)
 // Measured (kernel alone, one B200): 32 sequences of 256 to 2048, window 1024,
-// 40 heads, fp16: 94 us, 6.1 TB/s; 256 of 1000 to 32768, window 4096, 8 K/V
-// heads, bf16: 620 us, 6.7 TB/s; 128 of 1024 to 16384, 8 K/V heads, e4m3:
-// 370 to 400 us, 5.8 to 6.2 TB/s, where the conversions of codes take the ALU
-// 60 % of the time.  Small calls are bound by latency: lengths, table, tiles,
-// then the join, 14.5 us for one sequence and a window of 4100.
+// 40 heads, fp16: 89 us, 6.4 TB/s; 256 of 1000 to 32768, window 4096, 8 K/V
+// heads, bf16: 629 us, 6.6 TB/s; 128 of 1024 to 16384, 8 K/V heads, e4m3:
+// 370 us (405 on some runs), 6.2 TB/s, the same at 1530 and 1965 MHz, with the
+// ALU 37 % and the matrix unit 26 % busy.  Small calls are bound by latency:
+// lengths, table, tiles, then the join, 14.5 us for one sequence and a window
+// of 4100.
 //
 // Layout of the work: a "unit" is (sequence, K/V head, kHeads query heads);
 // its visible tokens are cut into tiles of 4 KB of K and 4 KB of V (16 tokens
@@ -43,12 +44,15 @@
 // times their mean.  Memory does not mind that a third of the warps have no
 // part, as long as the others end together, and a second segment or a
 // straddling unit costs a warp 4 us or more; the conversions of 8-bit codes
-// do mind.  Measured, parts against ranges (us, D = 128, 16 bits; units of 8
-// heads): 8 units of 4100 tokens 14.5 / 90; 128 of 4100 52 / 56 (single
-// warps 53); 256 of 4100 88 / 97; 1280 of 1028 109 / 112; 1280 of 256 to 1028
-// 94 / 102; but 384 of 512 to 4100 85 / 80, and 1024 of 1024 to 16384 in 8
-// bits 436 / 396.  8 units of 16 heads and 8000 tokens: CTAs 25, single warps
-// 57.
+// do mind.  Measured, parts against ranges (us, D = 128, 16 bits; units of up
+// to 8 heads): 8 units of 4100 tokens 14.3 / 88; 128 of 4100 50 / 60; 256 of
+// 4100 102 / 98; 1280 of 1028 108 / 115; 1280 of 256 to 1028 80 / 77; 1280 of
+// 256 to 1028, window 1024 (the 32 windows) 93 / 100; 384 of 512 to 4100 82 / 85.
+// Parts of up to 1.75 times a share in 8 bits against ranges (int8, e4m3): 1024
+// units of 1024 to 16384 584, 486 / 379, 375; like lengths, 1088 of 4000 256, 213
+// / 179, 186; 1088 of 9000 601, 521 / 386, 399; 1280 of 6000 415, 352 / 324, 325;
+// 320 of 8000 135, 116 / 113, 117; 1120 of 2000 131, 108 / 99, 105; 1280 of 1028
+// 71, 62 / 65, 64: hence 1.25 there.
 //
 // kHeads: groups of more than 8 heads take 16 columns at a time, which reads K
 // and V half as often (128 such units of 8000 tokens: 94 us against 131, 64 to

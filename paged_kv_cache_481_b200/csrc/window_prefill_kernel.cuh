@@ -12,11 +12,13 @@
 // and one exponential a pair on the special-function unit (16 a clock and
 // SM: as long as the matrix work at D = 128, twice as long at D = 64); for a
 // few queries a sequence, the read of K and V.
-// Measured (kernel alone, one B200): one prompt of 8192, window 4096, H 32,
-// KVH 8, bf16: 376 us, 1.10 PFLOP/s of visible pairs, two thirds of the library
-// product's rate; 8 chunks of 100 to 512 queries, 40 heads, fp16: 102 us, 4 to
-// 5 us of it between items; 16 sequences of 1 to 7 queries: 23 us, one wave of
-// dependent steps of 0.9 us.
+// Measured (one B200; long runs, where the power limit holds the clock near
+// 1725 MHz, and in brackets bursts at 1965 MHz): one prompt of 8192, window
+// 4096, H 32, KVH 8, bf16: 422 us (373), 0.98 PFLOP/s of visible pairs (1.10), 59
+// % of the library product's rate (67 %); 8 chunks of 100 to 512 queries, 40
+// heads, fp16: 112 us (100), 560 items where 396 would hold all rows, 4 to 5 us
+// between items; 16 sequences of 1 to 7 queries: 21.4 us, one wave of dependent
+// steps of 0.9 us with 4 to 28 of 256 rows in use.
 //
 // Layout of the work: the 128 rows of a query tile are tq = floor(128 / G)
 // tokens times the G query heads of one K/V head, so K and V are read once
@@ -51,7 +53,8 @@
 // type.  fp16: 2^7 times larger than the softmax's weights (below 2^15 with
 // the stale reference), which keeps weights down to 2^-31 of the largest.
 // bf16: small enough for the largest V (weight_shift in window_host.cuh).
-// The row sums are taken from the unrounded weights.
+// The row sums are taken from the unrounded weights.  (Two 16-bit numbers a
+// weight took 549 us against 438 on the prompt, 138 against 109 on the chunks.)
 #pragma once
 
 #include <cuda.h>
