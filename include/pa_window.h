@@ -179,7 +179,7 @@ PA_API pa_status pa_decode_q8(void *out, const void *q, const void *k_codes, con
  * A V row that is not finite, and that some query of its sequence sees, may
  * also reach queries less than 256 positions away from such a query, though
  * the mask hides it from them (a weight of zero times infinity is NaN); rows
- * that no query sees have no effect.  n_b > L_b or > max_query_len,
+ * that no query sees have no effect.  n_b < 0, > L_b or > max_query_len,
  * or rows outside q, are recorded (PA_DEVERR_CONTEXT_LEN) and that sequence
  * is skipped.
  */

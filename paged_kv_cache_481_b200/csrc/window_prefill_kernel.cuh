@@ -165,8 +165,10 @@ __device__ __forceinline__ int new_tokens(const WindowPrefillParams &p, int b, i
     L = p.lens[b];
     bad = L < 0 || L > p.max_len ? PA_DEVERR_CONTEXT_LEN : 0u;
     L = max(0, min(L, p.max_len));
-    if (n <= 0)
+    if (n <= 0) {
+        bad |= n < 0 ? PA_DEVERR_CONTEXT_LEN : 0u;
         return 0;
+    }
     if (first < 0 || n > p.num_rows - first || n > L || n > p.max_new) {
         bad = PA_DEVERR_CONTEXT_LEN;
         return 0;

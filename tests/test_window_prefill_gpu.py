@@ -272,3 +272,18 @@ def test_values_as_large_as_the_type_holds(lens, news, heads, kvh, d):
         out = _prefill(paged, q, news, 2500, 3, d ** -0.5)
         assert binding.pa_get_last_device_error() == 0
         _check(paged, q, out, news, 2500, 3, d ** -0.5)
+
+
+def test_starts_that_step_back_are_recorded():
+    """query_start_loc that decreases: its sequence has no rows (and others
+    may have the same ones twice), which the error word says."""
+    paged = Paged([50, 50, 50], 1, 64, 8, F16, seed=3, junk=0.0)
+    q = paged.randn((30, 2, 64))
+    binding.pa_get_last_device_error()
+    at = torch.tensor([0, 20, 15, 30], dtype=torch.int32).cuda()
+    out = _prefill(paged, q, [1], 100, 0, 0.1, starts=at, max_new=30)
+    assert binding.pa_get_last_device_error() == binding.PA_DEVERR_CONTEXT_LEN
+    k, v = paged.context64(2)
+    ref, mass = attend64(q[20:], k, v, range(40, 50), 100, 0, 0.1)
+    bound = attention_bound(ref, mass, F16, F16, float(v.abs().max()), 50)
+    assert bool(((out[20:].double() - ref).abs() <= bound).all())
