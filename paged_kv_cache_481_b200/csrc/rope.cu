@@ -82,13 +82,13 @@ cudaError_t launch_rope_q8(pa::RopeParams p, cudaStream_t stream)
 {
     constexpr int kRows = pa::kRopeThreads / (D / 16) * pa::kRopePasses, kSpan = 2 * 32 / (D / 16);
     p.groups = std::max((p.num_heads + kRows - 1) / kRows, (p.num_kv_heads + kSpan - 1) / kSpan);
-    p.check_blocks = p.num_blocks <= pa::kCheckFew * pa::kCheckParts ? pa::kCheckFew : pa::kCheckMany;
-    p.checkers = p.num_tokens > 1 ? 1 + (p.num_blocks - 1) / p.check_blocks : 0;
-    const int64_t ctas = int64_t(p.num_tokens) * p.groups + p.checkers;
+    p.scan_blocks = p.num_blocks <= pa::kScanFew * pa::kScanParts ? pa::kScanFew : pa::kScanMany;
+    p.scan_ctas = p.num_tokens > 1 ? 1 + (p.num_blocks - 1) / p.scan_blocks : 0;
+    const int64_t ctas = int64_t(p.num_tokens) * p.groups + p.scan_ctas;
     if (ctas > INT32_MAX)
         return cudaErrorInvalidValue;
     return launch_pdl(pa::rope_and_cache_q8_kernel<D, kBf16, kInterleaved, kE4m3>, dim3(unsigned(ctas)),
-                      dim3(pa::kRopeThreads), size_t(p.check_blocks) / 8, stream, p);
+                      dim3(pa::kRopeThreads), size_t(p.scan_blocks) / 8, stream, p);
 }
 
 } // namespace

@@ -42,7 +42,7 @@ struct RopeParams {
     int block_size, num_blocks;
     int scale_heads;                // heads of a block's scale row (kv heads rounded up to even)
     int groups;                     // 8-bit kernel: CTAs per token
-    int checkers, check_blocks;     // 8-bit kernel: CTAs that look for blocks with two runs, blocks of each
+    int scan_ctas, scan_blocks;     // 8-bit kernel: CTAs that look for blocks with two runs, blocks of each
     unsigned int *err;
 };
 
@@ -397,7 +397,7 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
         *my_scale = scale.scale;
 }
 
-// Records blocks from `first` on, p.check_blocks of them, that the call's tokens
+// Records blocks from `first` on, p.scan_blocks of them, that the call's tokens
 // enter more than once: a block's rows, older ones and scale are one run's to
 // write.  A bit a block, set by the first token of each run.  (A second one
 // whose position is outside the table is recorded for that.)
@@ -405,13 +405,15 @@ __device__ __forceinline__ void quantize_run(const RopeParams &p, int i0, int n,
 // parts, else 4 KB: next to 4 KB a CTA the L1 holds fewer of the rows that long
 // runs read twice (20 runs of 100 to 300 tokens, one K/V head: 25.6 us, with
 // 512 bytes or none 24.5), but every one of these CTAs passes over all slots,
-// and hundreds of them would be in the others' way.
-constexpr int kCheckFew = 4096, kCheckMany = 32768, kCheckParts = 64;
+// and hundreds of them would be in the others' way.  (10000 tokens of 7 heads
+// and one K/V head of 64, the most that this can weigh: 17.5 us without, 17.9
+// with 2000 blocks, 18.7 with 260,000, 18.3 with a million.)
+constexpr int kScanFew = 4096, kScanMany = 32768, kScanParts = 64;
 
-__device__ __forceinline__ void check_runs(const RopeParams &p, int64_t first, uint32_t *seen)
+__device__ __forceinline__ void scan_runs(const RopeParams &p, int64_t first, uint32_t *seen)
 {
     const int log2_bs = __ffs(p.block_size) - 1;
-    const int64_t blocks = min(int64_t(p.check_blocks), p.num_blocks - first);
+    const int64_t blocks = min(int64_t(p.scan_blocks), p.num_blocks - first);
     for (int i = threadIdx.x; i < (blocks + 31) / 32; i += kRopeThreads)
         seen[i] = 0;
     __syncthreads();
@@ -440,14 +442,14 @@ __device__ __forceinline__ void check_runs(const RopeParams &p, int64_t first, u
     }
 }
 
-// Grid: p.checkers CTAs, which look for blocks that two runs write (the call
-// takes no longer for them), then p.groups CTAs a token.  CTA g of them rotates the token's g-th 32
-// query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A token alone in
-// its run (a decode step) has its heads done side by side, D / 16 lanes each
-// for K and for V.  The heads of a longer run are shared out over the CTAs of
-// its first kSpan tokens, a CTA a head (64 threads K, 64 threads V).  The q
-// rows are rotated by the same CTAs: with CTAs of their own the streaming part
-// waited behind the dependent one (55 us against 39 on 12 chunks).
+// Grid: p.scan_ctas CTAs, which look for blocks that two runs write (0 to 2 % of
+// a call), then p.groups CTAs a token.  CTA g of them rotates the token's g-th
+// 32 query rows (64 at D = 64) and looks after its g-th kSpan K/V heads.  A
+// token alone in its run (a decode step) has its heads done side by side, D / 16
+// lanes each for K and for V.  The heads of a longer run are shared out over the
+// CTAs of its first kSpan tokens, a CTA a head (64 threads K, 64 threads V).
+// The q rows are rotated by the same CTAs: with CTAs of their own the streaming
+// part waited behind the dependent one (55 us against 39 on 12 chunks).
 template <int D, bool kBf16, bool kInterleaved, bool kE4m3>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(const RopeParams p)
 {
@@ -455,11 +457,11 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_and_cache_q8_kernel(cons
     extern __shared__ uint32_t seen[];
     grid_dependency_wait();
     allow_dependent_launch();
-    if (int(blockIdx.x) < p.checkers) {
-        check_runs(p, int64_t(blockIdx.x) * p.check_blocks, seen);
+    if (int(blockIdx.x) < p.scan_ctas) {
+        scan_runs(p, int64_t(blockIdx.x) * p.scan_blocks, seen);
         return;
     }
-    const int cta = int(blockIdx.x) - p.checkers;
+    const int cta = int(blockIdx.x) - p.scan_ctas;
     constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kSpan = 2 * kHeads;
     constexpr int kRows = kRopeThreads / kUnits * kRopePasses;
     const int i = cta / p.groups, g = cta % p.groups;
